@@ -22,7 +22,7 @@ __all__ = [
     "decode", "decode_workspace", "decode_plan", "decode_from_host", "decode_topv", "decode_topv_workspace",
     "prefill_causal", "device_status", "selftest_wait_timeout", "DiffqkvError", "Dims", "library_path",
     "decode_noalloc", "decode_append", "decode_paged", "prefill_causal_prefix", "fold_query", "workspace_status",
-    "decode_topv_paged", "augq_project", "prefill_causal_paged",
+    "decode_topv_paged", "augq_project", "prefill_causal_paged", "page_map", "kv8_pools", "kv8_store",
 ]
 
 library_path = _capi.LIB_PATH
@@ -391,6 +391,115 @@ def prefill_causal_paged(q, k_pages, v_pages, block_table, prefix_len: int, *, s
                                             int(prefix_len), S, _ptr(out), _ptr(status), _stream_ptr(stream))
     check(st, "diffqkv_prefill_causal_paged")
     return out
+
+
+def _cuda(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> ctypes.c_void_p:
+    """Address of a contiguous tensor of the given type and shape on the current device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+             page_size: int, num_pages: int, query_start: Optional[torch.Tensor] = None,
+             slot_map: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+             total_lens: Optional[torch.Tensor] = None, pages_used: Optional[torch.Tensor] = None, *,
+             capacity: Optional[int] = None, status: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """Block tables and slot maps of a serving step, built on the GPU from the requests' lengths.
+
+    seq_lens and new_lens int32 [B]: positions held and added; block_table int32 [B, max_blocks] gets the pages
+    that the new positions need, taken from the front of free_pages (int32) in the requests' order.  Returns
+    (query_start [B + 1], slot_map [capacity], positions [capacity], total_lens [B], pages_used [1]), all int32;
+    give them, or ``capacity`` (rows of the step's token buffer) to have them allocated.  A step that does not fit
+    ``capacity`` or ``free_pages`` is dropped as a whole and flagged (``diffqkv_page_map``)."""
+    i32 = torch.int32
+    B = seq_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    max_blocks = block_table.shape[1]
+    if slot_map is None:
+        if capacity is None:
+            raise ValueError("give slot_map, or capacity")
+        slot_map = torch.empty(int(capacity), dtype=i32, device=seq_lens.device)
+        if positions is None:
+            positions = torch.empty_like(slot_map)
+    cap = slot_map.numel()
+    if query_start is None:
+        query_start = torch.empty(B + 1, dtype=i32, device=seq_lens.device)
+    if total_lens is None:
+        total_lens = torch.empty(B, dtype=i32, device=seq_lens.device)
+    if pages_used is None:
+        pages_used = torch.empty(1, dtype=i32, device=seq_lens.device)
+    if status is not None:
+        _status_word(status)
+    st = lib().diffqkv_page_map(
+        B, _cuda(seq_lens, "seq_lens", i32, (B,)), _cuda(new_lens, "new_lens", i32, (B,)),
+        _cuda(block_table, "block_table", i32, (B, max_blocks)), max_blocks, page_size, num_pages,
+        _cuda(free_pages, "free_pages", i32, (free_pages.numel(),)), free_pages.numel(), cap,
+        _cuda(query_start, "query_start", i32, (B + 1,)), _cuda(slot_map, "slot_map", i32, (cap,)),
+        None if positions is None else _cuda(positions, "positions", i32, (cap,)),
+        _cuda(total_lens, "total_lens", i32, (B,)), _cuda(pages_used, "pages_used", i32, (1,)), _ptr(status),
+        _stream_ptr(stream))
+    check(st, "diffqkv_page_map")
+    return query_start, slot_map, positions, total_lens, pages_used
+
+
+def kv8_pools(num_pages: int, page_size: int, n_k: int, n_v: int, d_k: int, d_v: int, *,
+              scale_block: Optional[int] = None, device="cuda"):
+    """Empty pools of an 8-bit paged cache: (k_pages, v_pages, k_scales, v_scales).  Codes are zero-filled e4m3
+    [num_pages, page_size, heads, d]; scales uint8 [num_pages, page_size // scale_block, heads] (2^(byte - 127)),
+    one per page and head unless ``scale_block`` says otherwise."""
+    sb = page_size if scale_block is None else int(scale_block)
+    if sb < 1 or page_size % sb:
+        raise ValueError("scale_block must divide page_size")
+    out = [torch.zeros((num_pages, page_size, n, d), dtype=torch.float8_e4m3fn, device=device)
+           for n, d in ((n_k, d_k), (n_v, d_v))]
+    out += [torch.full((num_pages, page_size // sb, n), 127, dtype=torch.uint8, device=device) for n in (n_k, n_v)]
+    return tuple(out)
+
+
+def _kv8_cache(k_pages, v_pages, k_scales, v_scales):
+    """The C struct of an 8-bit cache, and (n_k, n_v, d_k, d_v)."""
+    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_scales.dim() != 3:
+        raise ValueError("k_pages / v_pages must be [num_pages, page_size, heads, d] and the scales "
+                         "[num_pages, page_size // scale_block, heads]")
+    num_pages, page_size, n_k, d_k = k_pages.shape
+    n_v, d_v = v_pages.shape[2], v_pages.shape[3]
+    parts = k_scales.shape[1]
+    if parts < 1 or page_size % parts:
+        raise ValueError("the scale blocks of k_scales do not divide the page")
+    e4m3, u8 = torch.float8_e4m3fn, torch.uint8
+    cache = _capi.Kv8Cache(
+        _cuda(k_pages, "k_pages", e4m3, k_pages.shape), _cuda(v_pages, "v_pages", e4m3, (num_pages, page_size, n_v, d_v)),
+        _cuda(k_scales, "k_scales", u8, (num_pages, parts, n_k)), _cuda(v_scales, "v_scales", u8, (num_pages, parts, n_v)),
+        num_pages, page_size, page_size // parts)
+    return cache, (n_k, n_v, d_k, d_v)
+
+
+def kv8_store(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, k_pages: torch.Tensor,
+              v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, *,
+              status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantises k_new [T, n_k, d_k] and v_new [T, n_v, d_v] (bf16) into the rows of an 8-bit cache that slot_map
+    (int32 [T], page * page_size + row, negative: skipped) names: e4m3 codes with a power-of-two scale for each block
+    of positions and head, grown when a later row needs it (``diffqkv_kv8_store``).  The tokens of a scale block must
+    be consecutive, as :func:`page_map` lays them out."""
+    cache, (n_k, n_v, d_k, d_v) = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
+    T = slot_map.numel()
+    if status is not None:
+        _status_word(status)
+    dims = Dims(1, n_k * n_v, n_k, n_v, d_k, d_v, 1.0)
+    st = lib().diffqkv_kv8_store(
+        dims, cache, _cuda(k_new, "k_new", torch.bfloat16, (T, n_k, d_k)),
+        _cuda(v_new, "v_new", torch.bfloat16, (T, n_v, d_v)), _cuda(slot_map, "slot_map", torch.int32, (T,)), T,
+        _ptr(status), _stream_ptr(stream))
+    check(st, "diffqkv_kv8_store")
 
 
 def _status_word(t: torch.Tensor):

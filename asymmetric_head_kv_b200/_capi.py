@@ -47,6 +47,18 @@ class Dims(ctypes.Structure):
     ]
 
 
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("scale_block", ctypes.c_int32),
+    ]
+
+
 class DecodeTuning(ctypes.Structure):
     _fields_ = [("grid_ctas", ctypes.c_int32), ("stages", ctypes.c_int32), ("ctas_per_sm", ctypes.c_int32)]
 
@@ -76,6 +88,7 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _DIMS = ctypes.POINTER(Dims)
+_KV8 = ctypes.POINTER(Kv8Cache)
 
 SIGNATURES = {
     "diffqkv_status_string": ([_I32], ctypes.c_char_p),
@@ -103,6 +116,8 @@ SIGNATURES = {
     "diffqkv_get_device_status": ([_P, ctypes.POINTER(_I32)], _I32),
     "diffqkv_selftest_wait_timeout": ([_I64, _P], _I32),
     "diffqkv_decode_noalloc": ([_DIMS, _P, _P, _P, _P, _I32, _I32, _P, _P], _I32),
+    "diffqkv_page_map": ([_I32, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "diffqkv_kv8_store": ([_DIMS, _KV8, _P, _P, _P, _I32, _P, _P], _I32),
     "diffqkv_fold_query": ([_DIMS, _I32, _I32, _P, _P, _P, _P], _I32),
 }
 

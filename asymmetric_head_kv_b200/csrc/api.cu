@@ -129,6 +129,25 @@ diffqkv_status_t make_tensor_map_3d(CUtensorMap *map, const void *base, uint64_t
     return r == CUDA_SUCCESS ? DIFFQKV_OK : DIFFQKV_ERR_INVALID_ARG;
 }
 
+diffqkv_status_t make_tensor_map_u8(CUtensorMap *map, const void *base, uint32_t rank, const uint64_t *dims,
+                                    const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle swizzle,
+                                    CUtensorMapL2promotion promotion) {
+    auto fn = encode_fn();
+    if (!fn) return DIFFQKV_ERR_CUDA;
+    if (rank < 3 || rank > 5) return DIFFQKV_ERR_INVALID_ARG;
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], estr[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) st[i] = strides_bytes[i];
+    }
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), d, st, bx, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DIFFQKV_OK : DIFFQKV_ERR_INVALID_ARG;
+}
+
 diffqkv_status_t ensure_dynamic_smem(const void *kernel, int bytes) {
     // cudaFuncSetAttribute costs host time on every call; remember what each
     // (kernel, device) pair has already been given
@@ -213,7 +232,7 @@ const char *diffqkv_status_string(int32_t status) {
     }
 }
 
-int32_t diffqkv_version(void) { return 10200; }
+int32_t diffqkv_version(void) { return 10300; }
 
 size_t diffqkv_decode_workspace_size(const diffqkv_dims_t *dims) { return diffqkv::decode_workspace_size(dims); }
 

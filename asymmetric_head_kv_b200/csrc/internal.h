@@ -41,6 +41,12 @@ diffqkv_status_t make_tensor_map_3d(CUtensorMap *map, const void *base, uint64_t
                                     uint32_t box0, uint32_t box1, uint32_t box2,
                                     CUtensorMapSwizzle swizzle);
 
+// Encodes a tiled tensor map of bytes (rank 3 to 5, dims[0] innermost and contiguous) with explicit byte
+// strides of dims 1 and up.
+diffqkv_status_t make_tensor_map_u8(CUtensorMap *map, const void *base, uint32_t rank, const uint64_t *dims,
+                                    const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle swizzle,
+                                    CUtensorMapL2promotion promotion);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Sets a kernel's dynamic shared-memory limit once per (kernel, device).
@@ -48,6 +54,9 @@ diffqkv_status_t ensure_dynamic_smem(const void *kernel, int bytes);
 
 // Shape checks common to every entry point.
 diffqkv_status_t validate_dims(const diffqkv_dims_t *d);
+
+// kv8_store.cu: checks of an 8-bit cache (dims, pools, page and block sizes).
+diffqkv_status_t validate_kv8(const diffqkv_dims_t *d, const diffqkv_kv8_cache_t *c);
 
 // decode.cu
 // A paged K/V cache: pools [num_pages, page_size, heads, d] for K and for V and

@@ -30,8 +30,8 @@
  *        workspace's first 32-bit word, read and cleared by
  *        diffqkv_workspace_status;
  *      - diffqkv_prefill_causal_ex, diffqkv_prefill_causal_paged,
- *        diffqkv_augq_project: the word the caller passes (NULL: the
- *        per-device word);
+ *        diffqkv_augq_project, diffqkv_page_map, diffqkv_kv8_store: the
+ *        word the caller passes (NULL: the per-device word);
  *      - every other call (prefill without a word, diffqkv_decode_noalloc,
  *        the wait self-test): the per-device word, read and cleared by
  *        diffqkv_get_device_status.
@@ -459,6 +459,99 @@ diffqkv_status_t diffqkv_prefill_causal_paged(const diffqkv_dims_t *dims, const 
                                               int32_t page_size, int32_t num_pages, int32_t prefix_len,
                                               int32_t seq_len, void *out, int32_t *device_status_word,
                                               diffqkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Serving step: page bookkeeping and the 8-bit paged cache (not on the     */
+/* pages; they store K and V in separate caches, section 3.4 Step 2)         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Block tables and slot maps of a serving step, from the requests' lengths.
+ *
+ *   seq_lens    [batch] int32   positions request b holds already (s_b)
+ *   new_lens    [batch] int32   positions it adds in this step (n_b; 0 allowed)
+ *   block_table [batch, max_blocks] int32, read and written: the first
+ *               ceil(s_b / page_size) entries of a row name the pages the request
+ *               holds; the call writes the entries up to ceil((s_b + n_b) / page_size)
+ *               and leaves the others as they are
+ *   free_pages  [num_free] int32   pool pages to hand out, taken from the front in
+ *               the requests' order (NULL allowed when num_free is 0)
+ *
+ *   query_start [batch + 1] int32   rows of request b in the step's token buffer:
+ *               query_start[b] .. query_start[b + 1] - 1
+ *   slot_map    [capacity] int32    page * page_size + row of every token, -1 behind
+ *               the last one (16-byte aligned)
+ *   positions   [capacity] int32    position of every token in its sequence, -1 behind
+ *               the last one (16-byte aligned; NULL: not written)
+ *   total_lens  [batch] int32       s_b + n_b
+ *   pages_used  [1] int32           pages taken from free_pages
+ *
+ * A request whose lengths are negative or exceed max_blocks * page_size adds
+ * nothing (its total is s_b held inside that range) and is flagged
+ * DIFFQKV_ERR_DEVICE_SEQLEN.  A step with more new positions than `capacity`
+ * (DIFFQKV_ERR_DEVICE_SEQLEN) or more new pages than num_free
+ * (DIFFQKV_ERR_DEVICE_PAGE) is dropped as a whole: no table entry is written, every
+ * slot and position is -1, pages_used and query_start are 0 and total_lens are the
+ * lengths held before.  A free or held page outside [0, num_pages) is flagged
+ * DIFFQKV_ERR_DEVICE_PAGE and its tokens' slots are -1.  Outputs must not overlap inputs
+ * (block_table aside) or one another.  One launch, no workspace; device_status_word as in
+ * diffqkv_prefill_causal_ex.  max_blocks * page_size and num_pages * page_size must
+ * fit in int32 and batch is at most 2^24 (else DIFFQKV_ERR_UNSUPPORTED); int32 arrays
+ * 4-byte aligned unless stated.
+ */
+diffqkv_status_t diffqkv_page_map(int32_t batch, const int32_t *seq_lens, const int32_t *new_lens,
+                                  int32_t *block_table, int32_t max_blocks, int32_t page_size, int32_t num_pages,
+                                  const int32_t *free_pages, int32_t num_free, int32_t capacity,
+                                  int32_t *query_start, int32_t *slot_map, int32_t *positions, int32_t *total_lens,
+                                  int32_t *pages_used, int32_t *device_status_word, diffqkv_stream_t stream);
+
+/*
+ * A paged K/V cache held in 8 bits: e4m3 codes and, for every block of scale_block
+ * positions of a page and head, one byte e standing for the scale 2^(e - 127).  The
+ * value of an element is code * 2^(e - 127); each such value is a bf16 number.  A scale
+ * byte is read as if held inside [7, 246] (2^-120 .. 2^119), the range the writer uses.
+ */
+typedef struct {
+    void *k_pages;      /* [num_pages, page_size, n_k, d_k] e4m3, 16-byte aligned */
+    void *v_pages;      /* [num_pages, page_size, n_v, d_v] e4m3, 16-byte aligned */
+    uint8_t *k_scales;  /* [num_pages, page_size / scale_block, n_k] */
+    uint8_t *v_scales;  /* [num_pages, page_size / scale_block, n_v] */
+    int32_t num_pages;
+    int32_t page_size;   /* a multiple of 8 (else DIFFQKV_ERR_UNSUPPORTED) */
+    int32_t scale_block; /* divides page_size (else DIFFQKV_ERR_INVALID_ARG) */
+} diffqkv_kv8_cache_t;
+
+/*
+ * Quantises new K and V rows into the pages their slots name.
+ *
+ *   k_new    [tokens, n_k, d_k]   bf16
+ *   v_new    [tokens, n_v, d_v]   bf16
+ *   slot_map [tokens] int32       page * page_size + row; a negative slot is skipped
+ *                                 (diffqkv_page_map writes such maps)
+ *
+ * For each scale block and head that the call's rows touch, with a the largest finite
+ * magnitude among them and e_new the least exponent in [-120, 119] with a <= 448 * 2^e_new: if
+ * the lowest row written is the block's first, its scale becomes 2^e_new; otherwise the
+ * larger of that and its old scale, and when this is larger than the old one the rows
+ * below the lowest one written are moved to it (code * 2^(e_old - e), to nearest even:
+ * exact down to the smallest normal code).  Rows above stay as they are.  Then
+ * code = e4m3(x * 2^-e), to nearest even.  Infinities become +-448 * 2^e, NaN stays NaN;
+ * neither takes part in a.  (Magnitudes above 448 * 2^119 become that.)  So a block is filled in the order of its rows, over as many
+ * calls as one likes; the values do not depend on how a block's rows are dealt out to
+ * calls beyond those roundings.
+ *
+ * The tokens of one scale block must be consecutive in the call (they are in the maps of
+ * diffqkv_page_map, where a request's tokens are consecutive and pages belong to one
+ * request); two separate stretches of one block, or one slot named twice, leave that
+ * block's codes and scale unspecified.  A slot >= num_pages * page_size is flagged
+ * DIFFQKV_ERR_DEVICE_PAGE and skipped.  dims->batch and scale are not used (they must
+ * still be valid).  tokens >= 0 (0: nothing is launched, the other pointers may be NULL).
+ * num_pages * page_size must fit in int32.  device_status_word as in
+ * diffqkv_prefill_causal_ex.
+ */
+diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache, const void *k_new,
+                                   const void *v_new, const int32_t *slot_map, int32_t tokens,
+                                   int32_t *device_status_word, diffqkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Device error word                                                        */
