@@ -23,6 +23,7 @@ __all__ = [
     "prefill_causal", "device_status", "selftest_wait_timeout", "DiffqkvError", "Dims", "library_path",
     "decode_noalloc", "decode_append", "decode_paged", "prefill_causal_prefix", "fold_query", "workspace_status",
     "decode_topv_paged", "augq_project", "prefill_causal_paged", "page_map", "kv8_pools", "kv8_store",
+    "decode_paged_kv8",
 ]
 
 library_path = _capi.LIB_PATH
@@ -500,6 +501,34 @@ def kv8_store(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, 
         _cuda(v_new, "v_new", torch.bfloat16, (T, n_v, d_v)), _cuda(slot_map, "slot_map", torch.int32, (T,)), T,
         _ptr(status), _stream_ptr(stream))
     check(st, "diffqkv_kv8_store")
+
+
+def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                     v_scales: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                     scale: Optional[float] = None, max_seq_len: Optional[int] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """:func:`decode` over an 8-bit paged cache: e4m3 pools k_pages [num_pages, page_size, n_k, d_k] and v_pages
+    [num_pages, page_size, n_v, d_v], scale bytes [num_pages, page_size // scale_block, heads], block_table int32
+    [B, max_blocks], seq_lens int32 [B].  Returns bf16 [B, n_q, d_v]."""
+    cache, (n_k, n_v, d_k, d_v) = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [B, n_q, d_k] and block_table [B, max_blocks]")
+    B, n_q, _ = q.shape
+    max_blocks = block_table.shape[1]
+    bf16 = torch.bfloat16
+    dims = Dims(B, n_q, n_k, n_v, d_k, d_v, d_k ** -0.5 if scale is None else scale)
+    if out is None:
+        out = torch.empty((B, n_q, d_v), dtype=bf16, device=q.device)
+    if workspace is None:
+        workspace = decode_workspace(dims, device=q.device)
+    st = lib().diffqkv_decode_paged_kv8(
+        dims, cache, _cuda(q, "q", bf16, (B, n_q, d_k)), _cuda(block_table, "block_table", torch.int32, (B, max_blocks)),
+        max_blocks, _cuda(seq_lens, "seq_lens", torch.int32, (B,)), 0 if max_seq_len is None else max_seq_len,
+        _cuda(out, "out", bf16, (B, n_q, d_v)), _cuda(workspace, "workspace", torch.uint8, workspace.shape),
+        workspace.numel(), _stream_ptr(stream))
+    check(st, "diffqkv_decode_paged_kv8")
+    return out
 
 
 def _status_word(t: torch.Tensor):

@@ -44,6 +44,7 @@
 #include <numeric>
 
 #include "common.cuh"
+#include "decode_walk.cuh"
 #include "internal.h"
 
 namespace diffqkv {
@@ -85,15 +86,6 @@ struct DecodeArgs {
     uint32_t sub_k_bytes = 0, sub_v_bytes = 0;
 };
 
-
-// Position of the tile walk: unit (b, g), tile i of nt, first global tile P.
-struct Walker {
-    int b, g, i, nt, T;
-    long long P;
-};
-
-__device__ __forceinline__ int clamp_len(int v, int t_max) { return v < 0 ? 0 : (v > t_max ? t_max : v); }
-
 // Block-table entry of logical page pi of sequence b, unchecked.
 __device__ __forceinline__ int page_entry(const DecodeArgs &a, int b, int pi) {
     return __ldg(a.block_table + (size_t)b * a.max_blocks + pi);
@@ -118,27 +110,6 @@ __device__ __forceinline__ long long cache_row(const DecodeArgs &a, int b, int p
     if (!a.block_table) return (long long)b * a.t_max + p;
     const int page = paged_page(a, b, p / a.page_size);
     return page < 0 ? -1 : (long long)page * a.page_size + p % a.page_size;
-}
-
-template <int TT>
-__device__ __forceinline__ void walker_advance(Walker &w, const DecodeArgs &a) {
-    if (++w.i < w.nt) return;
-    w.P += w.nt;
-    w.i = 0;
-    if (++w.g < a.n_k) return;
-    w.g = 0;
-    for (;;) {
-        if (++w.b >= a.batch) { w.nt = 0; return; }
-        w.T = clamp_len(__ldg(a.seq_lens + w.b), a.t_max);
-        w.nt = (w.T + TT - 1) / TT;
-        if (w.nt > 0) return;
-    }
-}
-
-// CTA that owns global tile t when N tiles are cut into G equal ranges
-// [floor(c N / G), floor((c+1) N / G)).
-__device__ __forceinline__ long long cta_of_tile(long long t, long long N, long long G) {
-    return ((t + 1) * G - 1) / N;
 }
 
 // x / sub_rows, x / page_size and x % page_size: shifts when they are powers of two (the producer
@@ -253,65 +224,7 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1)
     }
 
     // ---- prologue (warp 0): total tile count N, then the unit holding this CTA's first tile
-    if (warp == 0) {
-        long long acc = 0;
-        for (int base = 0; base < a.batch; base += 32) {
-            const int b = base + lane;
-            int nt = 0;
-            if (b < a.batch) {
-                const int raw = __ldg(a.seq_lens + b);
-                if (c == 0 && (raw < 0 || raw > a.t_max)) record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
-                nt = (clamp_len(raw, a.t_max) + TT - 1) / TT;
-            }
-            long long incl = (long long)nt * a.n_k;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            acc += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        const long long N = acc;
-        // never more CTAs than tiles: every CTA range is then non-empty
-        const long long Ge = N < G ? N : G;
-        const long long t_begin = (c < Ge) ? (c * N) / Ge : N;
-        long long P0 = 0;
-        int b0 = a.batch, g0 = 0, i0 = 0;
-        acc = 0;
-        bool found = false;
-        for (int base = 0; base < a.batch && !found && N > 0; base += 32) {
-            const int b = base + lane;
-            const int nt = b < a.batch ? (clamp_len(__ldg(a.seq_lens + b), a.t_max) + TT - 1) / TT : 0;
-            const long long w = (long long)nt * a.n_k;
-            long long incl = w;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            const long long excl = incl - w;
-            const bool hit = b < a.batch && nt > 0 && acc + excl <= t_begin && t_begin < acc + incl;
-            const unsigned m = __ballot_sync(0xffffffffu, hit);
-            if (m) {
-                const int L = __ffs(m) - 1;
-                const long long start = __shfl_sync(0xffffffffu, acc + excl, L);
-                const int ntL = __shfl_sync(0xffffffffu, nt, L);
-                const long long within = t_begin - start;
-                b0 = base + L;
-                g0 = (int)(within / ntL);
-                i0 = (int)(within % ntL);
-                P0 = start + (long long)g0 * ntL;
-                found = true;
-            }
-            acc += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) {
-            scan_s[0] = N;
-            scan_s[1] = P0;
-            scan_s[2] = ((long long)b0 << 32) | (unsigned)g0;
-            scan_s[3] = i0;
-        }
-    }
+    if (warp == 0) walker_scan<TT>(a, c, G, lane, scan_s);
     __syncthreads();
 
     const long long N = scan_s[0];

@@ -553,6 +553,28 @@ diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8
                                    const void *v_new, const int32_t *slot_map, int32_t tokens,
                                    int32_t *device_status_word, diffqkv_stream_t stream);
 
+/*
+ * diffqkv_decode over an 8-bit paged cache: one query token per sequence.
+ *
+ *   q           [B, n_q, d_k]           bf16
+ *   block_table [B, max_blocks] int32   position j of sequence b is row j % page_size of
+ *                                       pool page block_table[b][j / page_size]
+ *   seq_lens    [B] int32               positions attended, the step's own token included
+ *                                       if it has been stored (diffqkv_kv8_store)
+ *   out         [B, n_q, d_v]           bf16
+ *
+ * out[b,h] = sum_j softmax_j(scale q[b,h].k_j) v_j over the values k_j, v_j the cache
+ * stands for.  The codes go to the tensor cores as they are; the query and the softmax weights
+ * (times their V scales) are split into three e4m3 terms each: 12 significant bits, or 2^-28 of the
+ * head's largest where that is more.  All sums, maxima and weights are fp32.  Lengths, clamping, zero rows for length 0, max_seq_len, the workspace
+ * (diffqkv_decode_workspace_size) and its error word are those of diffqkv_decode; entries
+ * read, bad entries and shared pages those of diffqkv_decode_paged.
+ */
+diffqkv_status_t diffqkv_decode_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
+                                          const void *q, const int32_t *block_table, int32_t max_blocks,
+                                          const int32_t *seq_lens, int32_t max_seq_len, void *out, void *workspace,
+                                          size_t workspace_bytes, diffqkv_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Device error word                                                        */
 /* ------------------------------------------------------------------------ */
