@@ -120,15 +120,17 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
-// Three e4m3 terms of x (|x| <= 256): x ~ t0 + t1 / 32 + t2 / 1024, to 12 significant bits or 2^-20.
-__device__ __forceinline__ void split3(float x, uint32_t &t0, uint32_t &t1, uint32_t &t2) {
+// Three e4m3 terms of x and of y (|x|, |y| <= 256): x ~ t0 + t1 / 32 + t2 / 1024, to 12 significant bits or 2^-20.
+// x's terms are the low bytes.
+__device__ __forceinline__ void split3x2(float x, float y, uint32_t (&t)[3]) {
     float a, b;
-    t0 = e4m3x2(x, 0.f);
-    f16x2_to_floats(e4m3x2_to_f16x2(t0), a, b);
-    const float r1 = (x - a) * 32.f;
-    t1 = e4m3x2(r1, 0.f);
-    f16x2_to_floats(e4m3x2_to_f16x2(t1), a, b);
-    t2 = e4m3x2((r1 - a) * 32.f, 0.f);
+    t[0] = e4m3x2(x, y);
+    f16x2_to_floats(e4m3x2_to_f16x2(t[0]), a, b);
+    x = (x - a) * 32.f;
+    y = (y - b) * 32.f;
+    t[1] = e4m3x2(x, y);
+    f16x2_to_floats(e4m3x2_to_f16x2(t[1]), a, b);
+    t[2] = e4m3x2((x - a) * 32.f, (y - b) * 32.f);
 }
 
 // Shared-memory bookkeeping behind the tiles.  The MMA warp can be a tile (or unit) ahead of the softmax and the
@@ -138,7 +140,7 @@ struct Misc {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kMaxVSlots], v_empty[kMaxVSlots];
     uint64_t s_full[2], p_full[2], pv_done[2], q_ready[2], sc_full[kScaleWarps], sc_empty[kScaleWarps], mma_done;
     long long scan[4];
-    float4 red[2][16];       // [tile parity][head]: the four warps' maxima
+    float red[2][4][16];     // [tile parity][warp][head]: maxima
     float l_red[4][16];
     float q_scale[2][16];    // [unit parity][head]: scale * log2(e) * 2^(the query's exponent)
     float s_new[16];
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc &ms = *reinterpret_cast<Misc *>(smem + a.off_misc);
     volatile int *abort_flag = &ms.abort_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const long long G = a.grid, c = blockIdx.x;
 
     if (tid == 0) {
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ms.tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)ms.tmem_slot);
 
     const long long N = ms.scan[0];
     // sequences without positions: zero rows, dealt out over the CTAs
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     const long long Ge = N < G ? N : G;  // CTAs that own tiles
     const long long t_begin = c < Ge ? c * N / Ge : 0;
-    const int n_tiles = c < Ge ? (int)((c + 1) * N / Ge - t_begin) : 0;
+    const int n_tiles = uniform(c < Ge ? (int)((c + 1) * N / Ge - t_begin) : 0);
 
     Walker w;
     w.b = (int)(ms.scan[2] >> 32);
@@ -238,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.nt = (w.T + kTT - 1) / kTT;
 
     if (warp == kLoadWarp) {
-        // ======================= TMA producer: lane f loads sub-box f (sub_rows positions inside one page)
+        // ======================= TMA producer: sub-boxes of sub_rows positions inside one page, lane f holds the
+        // pool page of sub-box f
         auto subs = [&](const Walker &x) {
             const int v = min(kTT, x.T - x.i * kTT) + a.sub_rows - 1;
             return a.sub_shift >= 0 ? v >> a.sub_shift : v / a.sub_rows;
@@ -258,14 +261,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load_k = [&](int k, const Walker &x, int page) {
             if (k >= kKStages) mbar_wait_bounded(&ms.k_empty[ks], kp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
             if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-            const int n = subs(x);
-            if (lane == 0) mbar_arrive_expect_tx(&ms.k_full[ks], (uint32_t)(n * a.sub_rows * DK));
+            const int n = uniform(subs(x)), g = uniform(x.g);
+            const int p = x.i * kTT + lane * a.sub_rows;
+            const int row = p - div_page(a, p) * a.page_size;
+            if (elect_one()) mbar_arrive_expect_tx(&ms.k_full[ks], (uint32_t)(n * a.sub_rows * DK));
             __syncwarp();
-            if (lane < n) {
-                const int p = x.i * kTT + lane * a.sub_rows;
-                tma_load_4d(k_s + ks * K_TILE + lane * a.sub_rows * DK, &tm_k, &ms.k_full[ks], 0, x.g,
-                            p - div_page(a, p) * a.page_size, page);
+#pragma unroll 1
+            for (int f = 0; f < n; ++f) {
+                const int row_f = __shfl_sync(0xffffffffu, row, f), page_f = __shfl_sync(0xffffffffu, page, f);
+                if (elect_one())
+                    tma_load_4d(k_s + ks * K_TILE + f * a.sub_rows * DK, &tm_k, &ms.k_full[ks], 0, g, row_f, page_f);
             }
+            __syncwarp();
             if (++ks == kKStages) {
                 ks = 0;
                 kp ^= 1u;
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 issued_k = k + 2;
             }
-            const int n = subs(w), v0 = w.g * QPK / a.q_per_v;
+            const int n = uniform(subs(w)), v0 = uniform(w.g * QPK / a.q_per_v);
             const int p = w.i * kTT + lane * a.sub_rows;
             const int row = p - div_page(a, p) * a.page_size;
             for (int v = 0; v < a.vpg; ++v) {
@@ -299,12 +306,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&ms.v_full[vs], (uint32_t)(n * a.sub_rows * DV));
+                if (elect_one()) mbar_arrive_expect_tx(&ms.v_full[vs], (uint32_t)(n * a.sub_rows * DV));
                 __syncwarp();
                 // a group at the end may span fewer V heads than the widest one: the last is loaded again
-                if (lane < n)
-                    tma_load_4d(v_s + vs * V_TILE + lane * a.sub_rows * DV, &tm_v, &ms.v_full[vs], 0,
-                                min(v0 + v, a.n_v - 1), row, page);
+                const int head = min(v0 + v, a.n_v - 1);
+#pragma unroll 1
+                for (int f = 0; f < n; ++f) {
+                    const int row_f = __shfl_sync(0xffffffffu, row, f), page_f = __shfl_sync(0xffffffffu, page, f);
+                    if (elect_one())
+                        tma_load_4d(v_s + vs * V_TILE + f * a.sub_rows * DV, &tm_v, &ms.v_full[vs], 0, head, row_f, page_f);
+                }
+                __syncwarp();
                 ++issued_v;
                 if (++vs == a.v_slots) {
                     vs = 0;
@@ -321,7 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ======================= queries into terms, MMA issue
-        const uint32_t k_addr = smem_addr(k_s), v_addr = smem_addr(v_s), p_addr = smem_addr(p_s), q_addr = smem_addr(q_s);
+        // descriptors of the first slots; a slot, buffer or K step further is an addition in their address field
+        const uint64_t k_desc = row_desc<DK>(smem_addr(k_s), 16, 8 * DK), q_desc = row_desc<DK>(smem_addr(q_s), 16, 8 * DK);
+        // d_v = 64: both halves of the 128 lanes read the one 64-wide block (lbo 0)
+        const uint64_t v_desc = row_desc<DV>(smem_addr(v_s), 0, 8 * DV), p_desc = row_desc<128>(smem_addr(p_s), 16, 1024);
         constexpr uint32_t idesc_s = idesc_e4m3(kTT, NS, false);
         const uint32_t idesc_o = idesc_e4m3(128, a.blk_rows, true);
         const uint32_t t_o = tmem + 2 * NS;
@@ -352,13 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float f = exp2_int(max(se, -126));
                     uint32_t t[3] = {0, 0, 0};
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float v = (e & 1 ? bf16hi(x[e / 2]) : bf16lo(x[e / 2])) * f;
-                        uint32_t b0, b1, b2;
-                        split3(v, b0, b1, b2);
-                        t[0] |= (b0 & 0xffu) << (8 * e);
-                        t[1] |= (b1 & 0xffu) << (8 * e);
-                        t[2] |= (b2 & 0xffu) << (8 * e);
+                    for (int e = 0; e < V / 2; ++e) {
+                        uint32_t b[3];
+                        split3x2(bf16lo(x[e]) * f, bf16hi(x[e]) * f, b);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) t[i] |= b[i] << (16 * e);
                     }
 #pragma unroll
                     for (int i = 0; i < 3; ++i) {
@@ -379,12 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mbar_wait_bounded(&ms.k_full[ks], kp, a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t qa = q_addr + (unit & 1) * a.q_bytes;
+            const uint64_t kd = k_desc + (uint32_t)(ks * (K_TILE >> 4));
+            const uint64_t qd = q_desc + (uint32_t)uniform(unit & 1) * (a.q_bytes >> 4);
+            const uint32_t t_s = tmem + (uint32_t)((k & 1) * NS);
+            if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < DK / 32; ++s)
-                    umma_e4m3(tmem + (uint32_t)((k & 1) * NS), row_desc<DK>(k_addr + ks * K_TILE + s * 32, 16, 8 * DK),
-                              row_desc<DK>(qa + s * 32, 16, 8 * DK), idesc_s, s > 0 ? 1u : 0u);
+                for (int s = 0; s < DK / 32; ++s) umma_e4m3(t_s, kd + s * 2, qd + s * 2, idesc_s, s > 0 ? 1u : 0u);
                 umma_commit(&ms.s_full[k & 1]);
                 umma_commit(&ms.k_empty[ks]);
             }
@@ -402,7 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_bounded(&ms.p_full[k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             const int valid = min(kTT, w.T - w.i * kTT);
-            const bool fresh = k == 0 || w.i == 0;
+            const uint32_t onto = (uint32_t)uniform(k != 0 && w.i != 0);  // 0: the unit's first tile starts O
+            uint64_t pd = p_desc + (uint32_t)((k & 1) * (a.p_bytes >> 4));
+            uint32_t t_v = t_o;
+            int in_blk = 0;
             for (int v = 0; v < a.vpg; ++v) {
                 mbar_wait_bounded(&ms.v_full[vs], vp, a.wait_limit_ns, abort_flag, a.status);
                 if (valid < kTT) {
@@ -413,27 +429,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t pa = p_addr + (k & 1) * a.p_bytes + (uint32_t)(v / a.per_blk * a.blk_rows * 128);
+                const uint64_t vd = v_desc + (uint32_t)(vs * (V_TILE >> 4));
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < kTT / 32; ++s)
-                        // d_v = 64: both halves of the 128 lanes read the one 64-wide block (lbo 0)
-                        umma_e4m3(t_o + (uint32_t)(v * a.blk_rows),
-                                  row_desc<DV>(v_addr + vs * V_TILE + s * 32 * DV, 0, 8 * DV),
-                                  row_desc<128>(pa + s * 32, 16, 1024), idesc_o, fresh && s == 0 ? 0u : 1u);
+                        umma_e4m3(t_v, vd + s * (32 * DV >> 4), pd + s * 2, idesc_o, s > 0 ? 1u : onto);
                     umma_commit(&ms.v_empty[vs]);
                 }
                 __syncwarp();
+                t_v += (uint32_t)a.blk_rows;
+                if (++in_blk == a.per_blk) {  // the next V heads' weights lie in the next block of P rows
+                    in_blk = 0;
+                    pd += (uint32_t)(a.blk_rows * 128 >> 4);
+                }
                 if (++vs == a.v_slots) {
                     vs = 0;
                     vp ^= 1u;
                 }
             }
-            if (lane == 0) umma_commit(&ms.pv_done[k & 1]);
+            if (elect_one()) umma_commit(&ms.pv_done[k & 1]);
+            __syncwarp();
             walker_advance<kTT>(w, a);
         }
         if (n_tiles > 0) {
-            if (lane == 0) umma_commit(&ms.mma_done);
+            if (elect_one()) umma_commit(&ms.mma_done);
             __syncwarp();
             mbar_wait_bounded(&ms.mma_done, 0, a.wait_limit_ns, nullptr, a.status);
         }
@@ -503,7 +522,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int8_t *ke = reinterpret_cast<const int8_t *>(sc_s + slot * a.sc_bytes);
             const int8_t *ve = ke + kTT;
             const int *vmax = reinterpret_cast<const int *>(sc_s + slot * a.sc_bytes + kTT * (1 + a.vpg));
+            // every load of the tile's scales ahead of the byte stores below, which could alias them
             const float kf = exp2_int(ke[tid]);
+            float vx[QPK], vm[QPK];
+#pragma unroll
+            for (int h = 0; h < QPK; ++h) {
+                vx[h] = (float)ve[(where[h] >> 20) * kTT + tid] + kTop;
+                vm[h] = (float)vmax[where[h] >> 20];
+            }
             mbar_wait_bounded(&ms.s_full[k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             float s[QPK];
@@ -520,31 +546,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // the tile's maxima
+            {
+                float m[QPK];
 #pragma unroll
-            for (int h = 0; h < QPK; ++h) {
-                const float m = warp_max(s[h]);
-                if (lane == 0) reinterpret_cast<float *>(&ms.red[k & 1][h])[warp] = m;
+                for (int h = 0; h < QPK; ++h) m[h] = warp_max(s[h]);
+                if (lane == 0)
+#pragma unroll
+                    for (int h = 0; h < QPK; ++h) ms.red[k & 1][warp][h] = m[h];
             }
             named_barrier(1, kSoftmaxThreads);
             bool any = false;
             float alpha[QPK];
 #pragma unroll
             for (int h = 0; h < QPK; ++h) {
-                const float4 m4 = ms.red[k & 1][h];
-                const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                const float mt = fmaxf(fmax3f(ms.red[k & 1][0][h], ms.red[k & 1][1][h], ms.red[k & 1][2][h]),
+                                       ms.red[k & 1][3][h]);
                 const float m_new = mt == -INFINITY ? 0.f : mt;
-                const float r_new = m_new + (float)vmax[where[h] >> 20];
+                const float r_new = m_new + vm[h];
+                // start: the references begin here; else they move only where the tile exceeds them
+                const bool grow = start || r_new > R[h] || m_new > m_ref[h] + kMaxSlack;
+                const float r2 = start ? r_new : fmaxf(r_new, R[h]), m2 = start ? m_new : fmaxf(m_new, m_ref[h]);
                 alpha[h] = 1.f;
-                if (start) {
-                    m_ref[h] = m_new;
-                    R[h] = r_new;
-                } else if (r_new > R[h] || m_new > m_ref[h] + kMaxSlack) {
-                    const float r2 = fmaxf(r_new, R[h]), m2 = fmaxf(m_new, m_ref[h]);
-                    alpha[h] = fast_exp2(R[h] - r2);
-                    l[h] *= fast_exp2(m_ref[h] - m2);
+                if (grow) {
+                    if (!start) {
+                        alpha[h] = fast_exp2(R[h] - r2);
+                        l[h] *= fast_exp2(m_ref[h] - m2);
+                        any = true;
+                    }
                     R[h] = r2;
                     m_ref[h] = m2;
-                    any = true;
                 }
             }
             if (any) {  // the same in all 128 threads: O is final for tile k - 1, then its columns are rescaled
@@ -567,20 +597,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
             }
+            uint32_t terms[(QPK + 1) / 2][3];
+#pragma unroll
+            for (int h = 0; h < QPK; h += 2) {
+                const int h1 = h + 1 < QPK ? h + 1 : h;
+                l[h] += fast_exp2(s[h] - m_ref[h]);
+                if (h1 > h) l[h1] += fast_exp2(s[h1] - m_ref[h1]);
+                split3x2(fast_exp2(s[h] + (vx[h] - R[h])), fast_exp2(s[h1] + (vx[h1] - R[h1])), terms[h / 2]);
+            }
             // the P buffer was read by the P.V of tile k - 2
             if (k >= 2)
                 mbar_wait_bounded(&ms.pv_done[k & 1], (uint32_t)((k >> 1) - 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             uint8_t *pb = p_s + (k & 1) * a.p_bytes;
 #pragma unroll
             for (int h = 0; h < QPK; ++h) {
-                l[h] += fast_exp2(s[h] - m_ref[h]);
-                const float x = fast_exp2(s[h] + ((float)ve[(where[h] >> 20) * kTT + tid] + kTop - R[h]));
-                uint32_t t0, t1, t2;
-                split3(x, t0, t1, t2);
                 const int row = where[h] >> 10 & 1023;
-                pb[swizzled<128>(row, tid)] = (uint8_t)t0;
-                pb[swizzled<128>(row + 1, tid)] = (uint8_t)t1;
-                pb[swizzled<128>(row + 2, tid)] = (uint8_t)t2;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    pb[swizzled<128>(row + i, tid)] = (uint8_t)(terms[h / 2][i] >> (8 * (h & 1)));
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
