@@ -44,10 +44,10 @@ namespace {
 
 constexpr int kTT = 128;              // positions per tile
 constexpr int kSoftmaxThreads = 128;  // warps 0-3
-constexpr int kMmaWarp = 4, kLoadWarp = 5, kScaleWarp0 = 6, kScaleWarps = 4;
+constexpr int kMmaWarp = 4, kKWarp = 5, kVWarp = 6, kScaleWarp0 = 7, kScaleWarps = 3;
 constexpr int kThreads = 32 * (kScaleWarp0 + kScaleWarps);
-constexpr int kKStages = 3;
-constexpr int kMaxVSlots = 24;
+constexpr int kMaxVSlots = 12;
+constexpr int k_stages(int dk) { return dk == 64 ? 3 : 2; }
 constexpr int kGridMax = 2048;         // as in decode.cu: sizes the workspace
 constexpr int kHeader = 256;
 constexpr int kPad = 4;                // a partial record: o[d_v], m, l, pad, pad
@@ -65,13 +65,11 @@ struct Kv8Args {
     int32_t batch, n_q, n_k, n_v, t_max, max_blocks;
     int32_t page_size, page_shift, num_pages, sb, sub_rows, sub_shift;
     int32_t grid, vpg, q_per_v;
-    int32_t hv;        // most query heads of one V head inside a group
-    int32_t per_blk;   // V heads of one block of P rows
-    int32_t blk_rows;  // rows of a block: a multiple of 16
+    int32_t nb;        // blocks of four heads that one V head's query heads lie in, at most
     int32_t v_slots;
     uint32_t tmem_cols;
     uint32_t off_v, off_p, off_q, off_sc, off_misc;  // shared-memory layout
-    uint32_t p_bytes, q_bytes, sc_bytes;             // of one P buffer, q buffer, scale slot
+    uint32_t sc_bytes;                               // of one scale slot
     long long partial_slots, scale_blocks;
     float scale_log2;
     uint64_t wait_limit_ns;
@@ -93,8 +91,8 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
 }
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 A and B (format 0) and fp32 D.
-constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major) {
-    return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Shared-memory descriptor of rows of ROW bytes (64 or 128) in the swizzle of that width; `sbo`: bytes
@@ -106,7 +104,14 @@ __device__ __forceinline__ uint64_t row_desc(uint32_t saddr, uint32_t lbo, uint3
            ((uint64_t)((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | ((ROW == 128 ? 2ull : 4ull) << 61);
 }
 
-// Byte offset of byte c of row r in such a layout.
+// Shared-memory descriptor of an MN-major operand without swizzle: 16 bytes (along M or N) a row of K, rows one behind
+// another; `k_step`: bytes between groups of eight rows, `mn_step`: between 16-byte columns.
+__device__ __forceinline__ uint64_t flat_desc(uint32_t saddr, uint32_t k_step, uint32_t mn_step) {
+    return (uint64_t)((saddr >> 4) & 0x3fffu) | ((uint64_t)((k_step >> 4) & 0x3fffu) << 16) |
+           ((uint64_t)((mn_step >> 4) & 0x3fffu) << 32) | (1ull << 46);
+}
+
+// Byte offset of byte c of row r of a swizzled layout.
 template <int ROW>
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     const int x = ROW == 128 ? r & 7 : (r >> 1) & 3;
@@ -137,38 +142,33 @@ __device__ __forceinline__ void split3x2(float x, float y, uint32_t (&t)[3]) {
 // softmax two tiles ahead of the MMA warp's waits, so barriers between them alternate: each is completed again
 // only after its waiter has passed.
 struct Misc {
-    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kMaxVSlots], v_empty[kMaxVSlots];
+    uint64_t k_full[3], k_empty[3], v_full[kMaxVSlots], v_empty[kMaxVSlots];
     uint64_t s_full[2], p_full[2], pv_done[2], q_ready[2], sc_full[kScaleWarps], sc_empty[kScaleWarps], mma_done;
     long long scan[4];
     float red[2][4][16];     // [tile parity][warp][head]: maxima
     float l_red[4][16];
     float q_scale[2][16];    // [unit parity][head]: scale * log2(e) * 2^(the query's exponent)
-    float s_new[16];
     uint32_t tmem_slot;
     int abort_flag, last_flag;
 };
 
-// Where a query head's weights and outputs lie: its V head inside the group, its first P row, and its first O column.
-struct HeadSlot {
-    int vl, prow, ocol;
-};
-__device__ __forceinline__ HeadSlot head_slot(const Kv8Args &a, int g, int qpk, int h) {
-    const int first = g * qpk, abs = first + h;
-    const int v0 = first / a.q_per_v, v = abs / a.q_per_v;
-    HeadSlot s;
-    s.vl = v - v0;
-    const int in_blk = ((s.vl % a.per_blk) * a.hv + abs - max(first, v * a.q_per_v)) * 3;
-    s.prow = s.vl / a.per_blk * a.blk_rows + in_blk;
-    s.ocol = s.vl * a.blk_rows + in_blk;
-    return s;
+// Query heads of a group lie in blocks of four: head h's terms are columns (h / 4) * 16 + (h % 4) * 3 + term of S, of
+// the query operand and of P.  V head v of the group (v0 + v of the cache) multiplies `nb` blocks from this one on:
+__device__ __forceinline__ int first_block(const Kv8Args &a, int g, int qpk, int v) {
+    const int h0 = max(0, (g * qpk / a.q_per_v + v) * a.q_per_v - g * qpk);  // its first query head in the group
+    return min(h0 / 4, (qpk + 3) / 4 - a.nb);
 }
 
 template <int DK, int DV, int QPK>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     decode_kv8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const Kv8Args a) {
-    constexpr int NS = (3 * QPK + 15) / 16 * 16;  // S columns: column term * QPK + head
+    constexpr int NBLK = (QPK + 3) / 4;  // blocks of four heads
+    constexpr int NS = 16 * NBLK;        // S columns
     constexpr int K_TILE = kTT * DK, V_TILE = kTT * DV;
+    constexpr int KST = k_stages(DK);
+    constexpr uint32_t P_BLOCK = kTT * 16, P_BYTES = NBLK * P_BLOCK;  // a block of P: 16 bytes a position
+    constexpr uint32_t Q_BYTES = (NS * DK + 1023) / 1024 * 1024;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint8_t *k_s = smem, *v_s = smem + a.off_v, *p_s = smem + a.off_p, *q_s = smem + a.off_q, *sc_s = smem + a.off_sc;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long G = a.grid, c = blockIdx.x;
 
     if (tid == 0) {
-        for (int s = 0; s < kKStages; ++s) {
+        for (int s = 0; s < KST; ++s) {
             mbar_init(&ms.k_full[s], 1);
             mbar_init(&ms.k_empty[s], 1);
         }
@@ -202,17 +202,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ms.last_flag = 0;
         fence_barrier_init();
     }
-    if (warp == kLoadWarp && lane == 0) {
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
-    }
+    if (warp == kKWarp && lane == 0) prefetch_tensormap(&tm_k);
+    if (warp == kVWarp && lane == 0) prefetch_tensormap(&tm_v);
     if (warp == 0) walker_scan<kTT>(a, c, G, lane, ms.scan);
     if (warp == kMmaWarp) {
         tmem_alloc(&ms.tmem_slot, a.tmem_cols);
         tmem_relinquish();
     }
-    // unused P rows and query rows are operands too: start them from zero
-    for (uint32_t i = tid * 16; i < 2 * (a.p_bytes + a.q_bytes); i += kThreads * 16)
+    // unused columns of P and of the queries are operands too: start them from zero
+    for (uint32_t i = tid * 16; i < 2 * (P_BYTES + Q_BYTES); i += kThreads * 16)
         *reinterpret_cast<uint4 *>(p_s + i) = make_uint4(0, 0, 0, 0);  // (the q buffers follow the P buffers)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
@@ -239,9 +237,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.T = n_tiles ? clamp_len(__ldg(a.seq_lens + w.b), a.t_max) : 0;
     w.nt = (w.T + kTT - 1) / kTT;
 
-    if (warp == kLoadWarp) {
-        // ======================= TMA producer: sub-boxes of sub_rows positions inside one page, lane f holds the
-        // pool page of sub-box f
+    if (warp == kKWarp || warp == kVWarp) {
+        // ======================= TMA producers of the two rings: sub-boxes of sub_rows positions inside one page; lane f
+        // holds the pool page of sub-box f, fetched a tile ahead
+        const bool is_k = warp == kKWarp;
+        uint64_t *full = is_k ? ms.k_full : ms.v_full, *empty = is_k ? ms.k_empty : ms.v_empty;
+        uint8_t *ring = is_k ? k_s : v_s;
+        const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+        const int slots = is_k ? KST : a.v_slots, heads = is_k ? 1 : a.vpg;
+        const int tile_bytes = is_k ? K_TILE : V_TILE, box_bytes = a.sub_rows * (is_k ? DK : DV);
         auto subs = [&](const Walker &x) {
             const int v = min(kTT, x.T - x.i * kTT) + a.sub_rows - 1;
             return a.sub_shift >= 0 ? v >> a.sub_shift : v / a.sub_rows;
@@ -251,94 +255,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                        ? __ldg(a.block_table + (size_t)x.b * a.max_blocks + div_page(a, x.i * kTT + lane * a.sub_rows))
                        : 0;
         };
-        auto checked = [&](int page) {  // a bad entry (flagged) loads pool page 0: the loads stay in bounds
-            if (page >= 0 && page < a.num_pages) return page;
-            record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
-            return 0;
-        };
-        int ks = 0;             // K stage and its parity
-        uint32_t kp = 0;
-        auto load_k = [&](int k, const Walker &x, int page) {
-            if (k >= kKStages) mbar_wait_bounded(&ms.k_empty[ks], kp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-            const int n = uniform(subs(x)), g = uniform(x.g);
-            const int p = x.i * kTT + lane * a.sub_rows;
-            const int row = p - div_page(a, p) * a.page_size;
-            if (elect_one()) mbar_arrive_expect_tx(&ms.k_full[ks], (uint32_t)(n * a.sub_rows * DK));
-            __syncwarp();
-#pragma unroll 1
-            for (int f = 0; f < n; ++f) {
-                const int row_f = __shfl_sync(0xffffffffu, row, f), page_f = __shfl_sync(0xffffffffu, page, f);
-                if (elect_one())
-                    tma_load_4d(k_s + ks * K_TILE + f * a.sub_rows * DK, &tm_k, &ms.k_full[ks], 0, g, row_f, page_f);
+        int next = n_tiles ? entry(w) : 0;
+        int slot = 0, issued = 0;
+        uint32_t par = 0;
+        for (int k = 0; k < n_tiles; ++k) {
+            int page = next;
+            if (page < 0 || page >= a.num_pages) {  // a bad entry loads pool page 0: the loads stay in bounds
+                if (is_k) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+                page = 0;
             }
-            __syncwarp();
-            if (++ks == kKStages) {
-                ks = 0;
-                kp ^= 1u;
-            }
-            return true;
-        };
-        Walker wk = w;  // tile whose K is requested next
-        int page_k = n_tiles ? checked(entry(wk)) : 0;
-        int issued_k = 0;
-        long long issued_v = 0;
-        int vs = 0;
-        uint32_t vp = 0;
-        bool ok = n_tiles > 0 && load_k(0, wk, page_k);
-        if (ok) issued_k = 1;
-        for (int k = 0; k < n_tiles && ok; ++k) {
-            const int page = page_k;
-            if (k + 1 < n_tiles) {
-                walker_advance<kTT>(wk, a);
-                page_k = checked(entry(wk));
-                ok = load_k(k + 1, wk, page_k);
-                if (!ok) break;
-                issued_k = k + 2;
-            }
-            const int n = uniform(subs(w)), v0 = uniform(w.g * QPK / a.q_per_v);
+            const int n = uniform(subs(w));
+            const int h0 = uniform(is_k ? w.g : w.g * QPK / a.q_per_v), last = is_k ? a.n_k - 1 : a.n_v - 1;
             const int p = w.i * kTT + lane * a.sub_rows;
             const int row = p - div_page(a, p) * a.page_size;
-            for (int v = 0; v < a.vpg; ++v) {
-                if (issued_v >= a.v_slots)
-                    mbar_wait_bounded(&ms.v_empty[vs], vp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
+            walker_advance<kTT>(w, a);
+            if (k + 1 < n_tiles) next = entry(w);
+            for (int v = 0; v < heads; ++v) {
+                if (issued >= slots) mbar_wait_bounded(&empty[slot], par ^ 1u, a.wait_limit_ns, abort_flag, a.status);
                 if (__any_sync(0xffffffffu, *abort_flag != 0)) {
-                    ok = false;
+                    k = n_tiles;
                     break;
                 }
-                if (elect_one()) mbar_arrive_expect_tx(&ms.v_full[vs], (uint32_t)(n * a.sub_rows * DV));
+                if (elect_one()) mbar_arrive_expect_tx(&full[slot], (uint32_t)(n * box_bytes));
                 __syncwarp();
                 // a group at the end may span fewer V heads than the widest one: the last is loaded again
-                const int head = min(v0 + v, a.n_v - 1);
-#pragma unroll 1
+                const int head = min(h0 + v, last);
+                uint8_t *dst = ring + slot * tile_bytes;
+#pragma unroll 4
                 for (int f = 0; f < n; ++f) {
                     const int row_f = __shfl_sync(0xffffffffu, row, f), page_f = __shfl_sync(0xffffffffu, page, f);
-                    if (elect_one())
-                        tma_load_4d(v_s + vs * V_TILE + f * a.sub_rows * DV, &tm_v, &ms.v_full[vs], 0, head, row_f, page_f);
+                    if (elect_one()) tma_load_4d(dst + f * box_bytes, map, &full[slot], 0, head, row_f, page_f);
                 }
                 __syncwarp();
-                ++issued_v;
-                if (++vs == a.v_slots) {
-                    vs = 0;
-                    vp ^= 1u;
+                ++issued;
+                if (++slot == slots) {
+                    slot = 0;
+                    par ^= 1u;
                 }
             }
-            walker_advance<kTT>(w, a);
         }
-        if (lane == 0) {  // drain: no copy may still be landing when the CTA exits
-            for (int k = max(0, issued_k - kKStages); k < issued_k; ++k)
-                mbar_wait_bounded(&ms.k_full[k % kKStages], (uint32_t)(k / kKStages & 1), a.wait_limit_ns, nullptr, a.status);
-            for (long long k = issued_v > a.v_slots ? issued_v - a.v_slots : 0; k < issued_v; ++k)
-                mbar_wait_bounded(&ms.v_full[k % a.v_slots], (uint32_t)(k / a.v_slots & 1), a.wait_limit_ns, nullptr, a.status);
-        }
+        // drain: no copy may still be landing when the CTA exits
+        for (int k = max(0, issued - slots); k < issued; ++k)
+            mbar_wait_bounded(&full[k % slots], (uint32_t)(k / slots & 1), a.wait_limit_ns, nullptr, a.status);
     } else if (warp == kMmaWarp) {
         // ======================= queries into terms, MMA issue
         // descriptors of the first slots; a slot, buffer or K step further is an addition in their address field
         const uint64_t k_desc = row_desc<DK>(smem_addr(k_s), 16, 8 * DK), q_desc = row_desc<DK>(smem_addr(q_s), 16, 8 * DK);
         // d_v = 64: both halves of the 128 lanes read the one 64-wide block (lbo 0)
-        const uint64_t v_desc = row_desc<DV>(smem_addr(v_s), 0, 8 * DV), p_desc = row_desc<128>(smem_addr(p_s), 16, 1024);
-        constexpr uint32_t idesc_s = idesc_e4m3(kTT, NS, false);
-        const uint32_t idesc_o = idesc_e4m3(128, a.blk_rows, true);
+        const uint64_t v_desc = row_desc<DV>(smem_addr(v_s), 0, 8 * DV), p_desc = flat_desc(smem_addr(p_s), 128, P_BLOCK);
+        constexpr uint32_t idesc_s = idesc_e4m3(kTT, NS, false, false);
+        const uint32_t idesc_o = idesc_e4m3(128, 16 * a.nb, true, true);
         const uint32_t t_o = tmem + 2 * NS;
         Walker wk = w;      // tile whose S is issued next
         int unit = -1;      // its unit, counted from 0
@@ -347,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_s = [&](int k) {
             if (k == 0 || wk.i == 0) {
                 ++unit;
-                uint8_t *qb = q_s + (unit & 1) * a.q_bytes;
+                uint8_t *qb = q_s + (unit & 1) * Q_BYTES;
                 constexpr int V = DK / 32;
                 // amax of every head, its power-of-two scale (largest element into [128, 256)), and the three terms
 #pragma unroll (QPK < 4 ? QPK : 4)
@@ -375,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 3; ++i) {
-                        uint8_t *dst = qb + swizzled<DK>(i * QPK + h, lane * V);
+                        uint8_t *dst = qb + swizzled<DK>(h / 4 * 16 + h % 4 * 3 + i, lane * V);
                         if constexpr (V == 2)
                             *reinterpret_cast<uint16_t *>(dst) = (uint16_t)t[i];
                         else
@@ -393,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_bounded(&ms.k_full[ks], kp, a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             const uint64_t kd = k_desc + (uint32_t)(ks * (K_TILE >> 4));
-            const uint64_t qd = q_desc + (uint32_t)uniform(unit & 1) * (a.q_bytes >> 4);
+            const uint64_t qd = q_desc + (uint32_t)uniform(unit & 1) * (Q_BYTES >> 4);
             const uint32_t t_s = tmem + (uint32_t)((k & 1) * NS);
             if (elect_one()) {
 #pragma unroll
@@ -402,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(&ms.k_empty[ks]);
             }
             __syncwarp();
-            if (++ks == kKStages) {
+            if (++ks == KST) {
                 ks = 0;
                 kp ^= 1u;
             }
@@ -416,9 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int valid = min(kTT, w.T - w.i * kTT);
             const uint32_t onto = (uint32_t)uniform(k != 0 && w.i != 0);  // 0: the unit's first tile starts O
-            uint64_t pd = p_desc + (uint32_t)((k & 1) * (a.p_bytes >> 4));
+            const uint64_t p_buf = p_desc + (uint32_t)((k & 1) * (P_BYTES >> 4));
             uint32_t t_v = t_o;
-            int in_blk = 0;
             for (int v = 0; v < a.vpg; ++v) {
                 mbar_wait_bounded(&ms.v_full[vs], vp, a.wait_limit_ns, abort_flag, a.status);
                 if (valid < kTT) {
@@ -430,18 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint64_t vd = v_desc + (uint32_t)(vs * (V_TILE >> 4));
+                uint64_t pd = p_buf;
+                if constexpr (NBLK > 1) pd += (uint32_t)(uniform(first_block(a, w.g, QPK, v)) * (int)(P_BLOCK >> 4));
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < kTT / 32; ++s)
-                        umma_e4m3(t_v, vd + s * (32 * DV >> 4), pd + s * 2, idesc_o, s > 0 ? 1u : onto);
+                        umma_e4m3(t_v, vd + s * (32 * DV >> 4), pd + s * (32 * 16 >> 4), idesc_o, s > 0 ? 1u : onto);
                     umma_commit(&ms.v_empty[vs]);
                 }
                 __syncwarp();
-                t_v += (uint32_t)a.blk_rows;
-                if (++in_blk == a.per_blk) {  // the next V heads' weights lie in the next block of P rows
-                    in_blk = 0;
-                    pd += (uint32_t)(a.blk_rows * 128 >> 4);
-                }
+                t_v += (uint32_t)(16 * a.nb);
                 if (++vs == a.v_slots) {
                     vs = 0;
                     vp ^= 1u;
@@ -500,8 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ======================= softmax: thread tid owns position tid of a tile (TMEM lane tid)
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
         const uint32_t t_s = tmem + lane_base, t_o = tmem + 2 * NS + lane_base;
-        float m_ref[QPK], R[QPK], l[QPK], qs[QPK];
-        int where[QPK];  // vl << 20 | prow << 10 | ocol
+        auto o_column = [&](int h, int v, int g) {  // head h's first column of O, its V head being v
+            return (v * a.nb + h / 4 - first_block(a, g, QPK, v)) * 16 + h % 4 * 3;
+        };
+        float l[QPK];                    // this position's share of the row sums
+        float m_ref = 0.f, R = 0.f;      // lane h: head h's references (the same in the four warps)
+        int vl[QPK];                     // V head of each query head inside the group
         int unit = -1;
         for (int k = 0; k < n_tiles; ++k) {
             const bool start = k == 0 || w.i == 0;
@@ -509,11 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (start) {
                 ++unit;
                 mbar_wait_bounded(&ms.q_ready[unit & 1], (uint32_t)(unit >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
+                const int v0 = w.g * QPK / a.q_per_v;
 #pragma unroll
                 for (int h = 0; h < QPK; ++h) {
-                    qs[h] = ms.q_scale[unit & 1][h];
-                    const HeadSlot hs = head_slot(a, w.g, QPK, h);
-                    where[h] = hs.vl << 20 | hs.prow << 10 | hs.ocol;
+                    vl[h] = (w.g * QPK + h) / a.q_per_v - v0;
                     l[h] = 0.f;
                 }
             }
@@ -521,31 +487,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_bounded(&ms.sc_full[slot], (uint32_t)(k / kScaleWarps & 1), a.wait_limit_ns, abort_flag, a.status);
             const int8_t *ke = reinterpret_cast<const int8_t *>(sc_s + slot * a.sc_bytes);
             const int8_t *ve = ke + kTT;
-            const int *vmax = reinterpret_cast<const int *>(sc_s + slot * a.sc_bytes + kTT * (1 + a.vpg));
-            // every load of the tile's scales ahead of the byte stores below, which could alias them
             const float kf = exp2_int(ke[tid]);
-            float vx[QPK], vm[QPK];
+            float vx[QPK];
 #pragma unroll
-            for (int h = 0; h < QPK; ++h) {
-                vx[h] = (float)ve[(where[h] >> 20) * kTT + tid] + kTop;
-                vm[h] = (float)vmax[where[h] >> 20];
-            }
+            for (int h = 0; h < QPK; ++h) vx[h] = (float)ve[vl[h] * kTT + tid] + kTop;
+            const int my_vl = lane < QPK ? (w.g * QPK + lane) / a.q_per_v - w.g * QPK / a.q_per_v : 0;
+            const float vm = (float)reinterpret_cast<const int *>(sc_s + slot * a.sc_bytes + kTT * (1 + a.vpg))[my_vl];
             mbar_wait_bounded(&ms.s_full[k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             float s[QPK];
             {
-                uint32_t r[NS / 16][16];
+                uint32_t r[NBLK][16];
 #pragma unroll
-                for (int i = 0; i < NS / 16; ++i) tmem_ld_cols<16>(t_s + (uint32_t)((k & 1) * NS + i * 16), r[i]);
+                for (int i = 0; i < NBLK; ++i) tmem_ld_cols<16>(t_s + (uint32_t)((k & 1) * NS + i * 16), r[i]);
                 tmem_wait_ld();
-                auto col = [&](int i) { return __uint_as_float(r[i / 16][i % 16]); };
 #pragma unroll
                 for (int h = 0; h < QPK; ++h) {
-                    const float x = fmaf(fmaf(col(2 * QPK + h), 0.03125f, col(QPK + h)), 0.03125f, col(h));
-                    s[h] = tid < valid ? x * (qs[h] * kf) : -INFINITY;
+                    auto col = [&](int i) { return __uint_as_float(r[h / 4][h % 4 * 3 + i]); };
+                    const float x = fmaf(fmaf(col(2), 0.03125f, col(1)), 0.03125f, col(0));
+                    s[h] = tid < valid ? x * (ms.q_scale[unit & 1][h] * kf) : -INFINITY;
                 }
             }
-            // the tile's maxima
+            // the tile's maxima: across the warp by redux, across the warps through shared memory
             {
                 float m[QPK];
 #pragma unroll
@@ -555,67 +518,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < QPK; ++h) ms.red[k & 1][warp][h] = m[h];
             }
             named_barrier(1, kSoftmaxThreads);
-            bool any = false;
-            float alpha[QPK];
-#pragma unroll
-            for (int h = 0; h < QPK; ++h) {
+            // lane h moves head h's references where the tile exceeds them
+            float alpha = 1.f, l_scale = 1.f;
+            {
+                const int h = lane < QPK ? lane : 0;
                 const float mt = fmaxf(fmax3f(ms.red[k & 1][0][h], ms.red[k & 1][1][h], ms.red[k & 1][2][h]),
                                        ms.red[k & 1][3][h]);
-                const float m_new = mt == -INFINITY ? 0.f : mt;
-                const float r_new = m_new + vm[h];
-                // start: the references begin here; else they move only where the tile exceeds them
-                const bool grow = start || r_new > R[h] || m_new > m_ref[h] + kMaxSlack;
-                const float r2 = start ? r_new : fmaxf(r_new, R[h]), m2 = start ? m_new : fmaxf(m_new, m_ref[h]);
-                alpha[h] = 1.f;
-                if (grow) {
-                    if (!start) {
-                        alpha[h] = fast_exp2(R[h] - r2);
-                        l[h] *= fast_exp2(m_ref[h] - m2);
-                        any = true;
-                    }
-                    R[h] = r2;
-                    m_ref[h] = m2;
+                const float m_new = mt == -INFINITY ? 0.f : mt, r_new = m_new + vm;
+                if (start) {
+                    m_ref = m_new;
+                    R = r_new;
+                } else if (r_new > R || m_new > m_ref + kMaxSlack) {
+                    const float r2 = fmaxf(r_new, R), m2 = fmaxf(m_new, m_ref);
+                    alpha = fast_exp2(R - r2);
+                    l_scale = fast_exp2(m_ref - m2);
+                    R = r2;
+                    m_ref = m2;
                 }
             }
-            if (any) {  // the same in all 128 threads: O is final for tile k - 1, then its columns are rescaled
+            if (__any_sync(0xffffffffu, alpha != 1.f || l_scale != 1.f)) {
+                // (the same in all four warps) O is final for tile k - 1, then the heads' columns are rescaled
                 mbar_wait_bounded(&ms.pv_done[(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
                                   a.status);
                 tc_fence_after();
 #pragma unroll
                 for (int h = 0; h < QPK; ++h) {
-                    if (alpha[h] == 1.f) continue;
-                    const uint32_t at = t_o + (uint32_t)(where[h] & 1023);
+                    l[h] *= __shfl_sync(0xffffffffu, l_scale, h);
+                    const float f = __shfl_sync(0xffffffffu, alpha, h);
+                    if (f == 1.f) continue;
+                    const uint32_t at = t_o + (uint32_t)o_column(h, vl[h], w.g);
                     uint32_t r[2], r2[1];
                     tmem_ld_cols<2>(at, r);
                     tmem_ld_cols<1>(at + 2, r2);
                     tmem_wait_ld();
-                    r[0] = __float_as_uint(__uint_as_float(r[0]) * alpha[h]);
-                    r[1] = __float_as_uint(__uint_as_float(r[1]) * alpha[h]);
-                    r2[0] = __float_as_uint(__uint_as_float(r2[0]) * alpha[h]);
+                    r[0] = __float_as_uint(__uint_as_float(r[0]) * f);
+                    r[1] = __float_as_uint(__uint_as_float(r[1]) * f);
+                    r2[0] = __float_as_uint(__uint_as_float(r2[0]) * f);
                     tmem_st_cols<2>(at, r);
                     tmem_st_cols<1>(at + 2, r2);
                 }
                 tmem_wait_st();
             }
-            uint32_t terms[(QPK + 1) / 2][3];
+            uint4 pk[NBLK];  // this position's row of each block: terms of heads 4 i, 4 i + 1, ... in bytes 0 .. 11
 #pragma unroll
-            for (int h = 0; h < QPK; h += 2) {
-                const int h1 = h + 1 < QPK ? h + 1 : h;
-                l[h] += fast_exp2(s[h] - m_ref[h]);
-                if (h1 > h) l[h1] += fast_exp2(s[h1] - m_ref[h1]);
-                split3x2(fast_exp2(s[h] + (vx[h] - R[h])), fast_exp2(s[h1] + (vx[h1] - R[h1])), terms[h / 2]);
+            for (int i = 0; i < NBLK; ++i) {
+                uint32_t t[2][3] = {{0, 0, 0}, {0, 0, 0}};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int h0 = 4 * i + 2 * j, h1 = h0 + 1 < QPK ? h0 + 1 : h0;
+                    if (h0 >= QPK) continue;
+                    const float m0 = __shfl_sync(0xffffffffu, m_ref, h0), r0 = __shfl_sync(0xffffffffu, R, h0);
+                    const float m1 = __shfl_sync(0xffffffffu, m_ref, h1), r1 = __shfl_sync(0xffffffffu, R, h1);
+                    l[h0] += fast_exp2(s[h0] - m0);
+                    if (h1 > h0) l[h1] += fast_exp2(s[h1] - m1);
+                    split3x2(fast_exp2(s[h0] + (vx[h0] - r0)), fast_exp2(s[h1] + (vx[h1] - r1)), t[j]);
+                }
+                // (t[j][i]: term i of heads 2 j and 2 j + 1 of the block)  head 0: bytes 0-2, head 1: 3-5, head 2: 6-8, ...
+                pk[i].x = (t[0][0] & 0xffu) | (t[0][1] & 0xffu) << 8 | (t[0][2] & 0xffu) << 16 | (t[0][0] >> 8) << 24;
+                pk[i].y = (t[0][1] >> 8) | (t[0][2] >> 8) << 8 | (t[1][0] & 0xffu) << 16 | (t[1][1] & 0xffu) << 24;
+                pk[i].z = (t[1][2] & 0xffu) | (t[1][0] >> 8) << 8 | (t[1][1] >> 8) << 16 | (t[1][2] >> 8) << 24;
+                pk[i].w = 0u;
             }
             // the P buffer was read by the P.V of tile k - 2
             if (k >= 2)
                 mbar_wait_bounded(&ms.pv_done[k & 1], (uint32_t)((k >> 1) - 1 & 1), a.wait_limit_ns, abort_flag, a.status);
-            uint8_t *pb = p_s + (k & 1) * a.p_bytes;
+            uint4 *pb = reinterpret_cast<uint4 *>(p_s + (k & 1) * P_BYTES) + tid;
 #pragma unroll
-            for (int h = 0; h < QPK; ++h) {
-                const int row = where[h] >> 10 & 1023;
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    pb[swizzled<128>(row + i, tid)] = (uint8_t)(terms[h / 2][i] >> (8 * (h & 1)));
-            }
+            for (int i = 0; i < NBLK; ++i) pb[i * kTT] = pk[i];
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             __syncwarp();
@@ -641,15 +610,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < QPK; ++h) {
                     uint32_t r[4];
-                    tmem_ld_cols<4>(t_o + (uint32_t)(where[h] & 1023), r);
+                    tmem_ld_cols<4>(t_o + (uint32_t)o_column(h, vl[h], w.g), r);
                     tmem_wait_ld();
                     const float o = fmaf(fmaf(__uint_as_float(r[2]), 0.03125f, __uint_as_float(r[1])), 0.03125f,
                                          __uint_as_float(r[0]));
                     float *dst = a.partials + ((size_t)(u + c) * QPK + h) * (DV + kPad);
+                    const float m_h = __shfl_sync(0xffffffffu, m_ref, h), r_h = __shfl_sync(0xffffffffu, R, h);
                     if (slot_ok) {
-                        if (tid < DV) __stcg(dst + tid, o * exp2f(R[h] - kTop - m_ref[h]));
+                        if (tid < DV) __stcg(dst + tid, o * exp2f(r_h - kTop - m_h));
                         if (tid == 0) {
-                            __stcg(dst + DV, m_ref[h]);
+                            __stcg(dst + DV, m_h);
                             __stcg(dst + DV + 1, ms.l_red[0][h] + ms.l_red[1][h] + ms.l_red[2][h] + ms.l_red[3][h]);
                         }
                     }
@@ -777,36 +747,37 @@ diffqkv_status_t decode_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_ca
     Kv8Args a;
     const int qpk = d->n_q / d->n_k, qpv = d->n_q / d->n_v;
     int span = 1;
-    a.hv = 1;
+    a.nb = 1;
     for (int g = 0; g < d->n_k; ++g) {
         const int v0 = g * qpk / qpv, v1 = ((g + 1) * qpk - 1) / qpv;
         span = std::max(span, v1 - v0 + 1);
-        for (int v = v0; v <= v1; ++v)
-            a.hv = std::max(a.hv, std::min((g + 1) * qpk, (v + 1) * qpv) - std::max(g * qpk, v * qpv));
+        for (int v = v0; v <= v1; ++v) {
+            const int h0 = std::max(0, v * qpv - g * qpk), h1 = std::min(qpk, (v + 1) * qpv - g * qpk) - 1;
+            a.nb = std::max(a.nb, h1 / 4 - h0 / 4 + 1);
+        }
     }
     a.vpg = span;
     a.q_per_v = qpv;
-    a.per_blk = a.hv <= 5 ? 5 / a.hv : 1;
-    a.blk_rows = (int)align_to((uint32_t)(3 * a.hv * a.per_blk), 16);
-    const int ns = (int)align_to((uint32_t)(3 * qpk), 16);
-    const int cols = 2 * ns + span * a.blk_rows;
+    const int ns = (qpk + 3) / 4 * 16, cols = 2 * ns + span * a.nb * 16;
     a.tmem_cols = 32;
-    while ((int)a.tmem_cols < cols + 1) a.tmem_cols *= 2;  // (+ 1: the last head's O is read four columns wide)
+    while ((int)a.tmem_cols < cols) a.tmem_cols *= 2;
     if (a.tmem_cols > 512) return DIFFQKV_ERR_UNSUPPORTED;
+    // two CTAs a SM, so that one's latencies (barriers, TMEM, conversions) hide behind the other's; one where TMEM does
+    // not hold two
+    const int per_sm = a.tmem_cols > 256 ? 1 : 2;
 
     // shared memory: K ring, V ring (what is left, at most kMaxVSlots slots), P and q buffers, scales, bookkeeping
     const uint32_t v_tile = (uint32_t)(kTT * d->d_v);
-    a.off_v = (uint32_t)(kKStages * kTT * d->d_k);
-    a.p_bytes = (uint32_t)((span + a.per_blk - 1) / a.per_blk * a.blk_rows * 128);
-    a.q_bytes = align_to((uint32_t)(ns * d->d_k), 1024);
+    const uint32_t p_bytes = (uint32_t)(ns * kTT), q_bytes = align_to((uint32_t)(ns * d->d_k), 1024);
+    a.off_v = (uint32_t)(k_stages(d->d_k) * kTT * d->d_k);
     a.sc_bytes = align_to((uint32_t)(kTT * (1 + span) + 4 * span), 16);
-    const uint32_t tail = 2 * a.p_bytes + 2 * a.q_bytes + kScaleWarps * a.sc_bytes + align_to((uint32_t)sizeof(Misc), 16);
-    const uint32_t room = 227 * 1024 - 1024 - a.off_v - tail;
+    const uint32_t tail = 2 * p_bytes + 2 * q_bytes + kScaleWarps * a.sc_bytes + align_to((uint32_t)sizeof(Misc), 16);
+    const uint32_t room = (per_sm == 2 ? 113u : 227u) * 1024 - 1024 - a.off_v - tail;
     a.v_slots = std::min<int>(kMaxVSlots, (int)(room / v_tile));
     if (a.v_slots < 2) return DIFFQKV_ERR_UNSUPPORTED;
     a.off_p = a.off_v + (uint32_t)a.v_slots * v_tile;
-    a.off_q = a.off_p + 2 * a.p_bytes;
-    a.off_sc = a.off_q + 2 * a.q_bytes;
+    a.off_q = a.off_p + 2 * p_bytes;
+    a.off_sc = a.off_q + 2 * q_bytes;
     a.off_misc = a.off_sc + kScaleWarps * a.sc_bytes;
     const uint32_t smem = a.off_p + tail + 1024;
 
@@ -850,10 +821,10 @@ diffqkv_status_t decode_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_ca
     a.scale_blocks = (long long)cache->num_pages * (P / cache->scale_block);
     a.scale_log2 = (float)((double)d->scale * 1.4426950408889634);
     a.wait_limit_ns = kWaitLimitNs;
-    // one CTA a SM, fewer where the hint says that there are fewer tiles
+    // fewer CTAs where the hint says that there are fewer tiles
     const int msl = max_seq_len >= 1 && max_seq_len <= a.t_max ? max_seq_len : a.t_max;
     const long long tiles = (long long)units * ((msl + kTT - 1) / kTT);
-    a.grid = (int)std::min<long long>({tiles, (long long)dev.num_sms, (long long)kGridMax});
+    a.grid = (int)std::min<long long>({tiles, (long long)dev.num_sms * per_sm, (long long)kGridMax});
     if (ensure_dynamic_smem((const void *)fn, (int)smem) != DIFFQKV_OK) return DIFFQKV_ERR_CUDA;
     fn<<<a.grid, kThreads, smem, stream>>>(tm_k, tm_v, a);
     return cudaGetLastError() == cudaSuccess ? DIFFQKV_OK : DIFFQKV_ERR_CUDA;
