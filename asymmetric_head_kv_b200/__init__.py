@@ -23,7 +23,7 @@ __all__ = [
     "prefill_causal", "device_status", "selftest_wait_timeout", "DiffqkvError", "Dims", "library_path",
     "decode_noalloc", "decode_append", "decode_paged", "prefill_causal_prefix", "fold_query", "workspace_status",
     "decode_topv_paged", "augq_project", "prefill_causal_paged", "page_map", "kv8_pools", "kv8_store",
-    "decode_paged_kv8",
+    "decode_paged_kv8", "prefill_paged_kv8", "prefill_paged_kv8_workspace",
 ]
 
 library_path = _capi.LIB_PATH
@@ -528,6 +528,43 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         _cuda(out, "out", bf16, (B, n_q, d_v)), _cuda(workspace, "workspace", torch.uint8, workspace.shape),
         workspace.numel(), _stream_ptr(stream))
     check(st, "diffqkv_decode_paged_kv8")
+    return out
+
+
+def prefill_paged_kv8_workspace(dims: Dims, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for :func:`prefill_paged_kv8` (reusable across calls, whatever their sizes)."""
+    n = lib().diffqkv_prefill_paged_kv8_workspace_size(dims)
+    if n == 0:
+        raise DiffqkvError(_capi.INVALID_ARG, "prefill_paged_kv8_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def prefill_paged_kv8(q: torch.Tensor, query_start: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      k_scales: torch.Tensor, v_scales: torch.Tensor, block_table: torch.Tensor,
+                      seq_lens: torch.Tensor, *, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention of a ragged batch of query rows over an 8-bit paged cache: q [tokens, n_q, d_k] bf16, request b
+    owning rows query_start[b] .. query_start[b + 1] - 1 (int32 [B + 1], as :func:`page_map` writes it) at the last
+    positions of its seq_lens[b] (int32 [B], the new rows included and stored).  Returns bf16 [tokens, n_q, d_v]; rows
+    behind query_start[B] are not written."""
+    cache, (n_k, n_v, d_k, d_v) = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [tokens, n_q, d_k] and block_table [B, max_blocks]")
+    T, n_q, _ = q.shape
+    B, max_blocks = block_table.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    dims = Dims(B, n_q, n_k, n_v, d_k, d_v, d_k ** -0.5 if scale is None else scale)
+    if out is None:
+        out = torch.empty((T, n_q, d_v), dtype=bf16, device=q.device)
+    if workspace is None:
+        workspace = prefill_paged_kv8_workspace(dims, q.device)
+    st = lib().diffqkv_prefill_paged_kv8(
+        dims, cache, _cuda(q, "q", bf16, (T, n_q, d_k)), _cuda(query_start, "query_start", i32, (B + 1,)), T,
+        _cuda(block_table, "block_table", i32, (B, max_blocks)), max_blocks, _cuda(seq_lens, "seq_lens", i32, (B,)),
+        _cuda(out, "out", bf16, (T, n_q, d_v)), _cuda(workspace, "workspace", torch.uint8, workspace.shape),
+        workspace.numel(), _stream_ptr(stream))
+    check(st, "diffqkv_prefill_paged_kv8")
     return out
 
 

@@ -119,6 +119,8 @@ SIGNATURES = {
     "diffqkv_page_map": ([_I32, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P], _I32),
     "diffqkv_kv8_store": ([_DIMS, _KV8, _P, _P, _P, _I32, _P, _P], _I32),
     "diffqkv_decode_paged_kv8": ([_DIMS, _KV8, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P], _I32),
+    "diffqkv_prefill_paged_kv8_workspace_size": ([_DIMS], _SZ),
+    "diffqkv_prefill_paged_kv8": ([_DIMS, _KV8, _P, _P, _I32, _P, _I32, _P, _P, _P, _SZ, _P], _I32),
     "diffqkv_fold_query": ([_DIMS, _I32, _I32, _P, _P, _P, _P], _I32),
 }
 

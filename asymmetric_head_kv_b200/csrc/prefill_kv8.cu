@@ -1,0 +1,796 @@
+// prefill_kv8.cu -- causal attention of a ragged batch of query rows over an 8-bit paged cache.
+//
+//   out[r, h] = sum_{j <= p_r} softmax_j(scale q[r, h] . k_j) v_j,   k_j = kc_j 2^ke_j,  v_j = vc_j 2^ve_j
+//
+// with p_r the row's position, kc, vc the e4m3 codes and ke, ve the exponents of their blocks.  A dense contraction,
+// 2 (d_k + d_v) operations for every row, head and position, on tcgen05 kind::f16:
+//
+//  * One CTA takes 256 query rows of one request and head as two 128-row tiles that share every 64-position K/V
+//    tile.  Four warps turn a tile's codes into f16 once for both: code * 2^(e - e_ref), with e_ref the tile's largest
+//    exponent for K and the largest so far for V, which is exact unless a block's scale is 2^15 below it.  (Feeding codes to fp8 MMAs instead
+//    would split every softmax weight into e4m3 terms, five more instructions for each pair of scores in the warps that
+//    bound this kernel; conversion costs the tile 12 instructions for 16 codes in warps that have nothing else
+//    to do.)  K's e_ref goes into the scores' multiplier; when V's grows, O is rescaled.
+//  * Queries are scaled by a power of two per row into f16's range (8 significant bits fit its 11).
+//  * Softmax warps own a row per thread; S is double-buffered in TMEM, P (f16) goes back over S and is the A
+//    operand of P.V; O is rescaled in TMEM only when a row's maximum grows by 2^8 or V's exponent grows.
+//    Weights are held at 2^7 of the reference, so that f16 resolves 2^-31 of the largest.
+//  * MMA, commit and TMA are issued by an elected lane (kv8.cuh).
+//  * Few rows over a long context: the K/V tiles of a unit are cut into equal splits over the SMs that have no unit of
+//    their own; partials in the workspace, merged by the last CTA of the unit.
+// What bounds it: the 64 exponentials a row and tile (16 a clock and SM) and the softmax warps' latencies.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+#include <numeric>
+
+#include "internal.h"
+#include "kv8.cuh"
+
+namespace diffqkv {
+
+namespace {
+
+constexpr int BM = 128, QT = 2, BN = 64;
+constexpr int kRows = QT * BM;
+constexpr int kSoftmaxWarps = 4 * QT;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kConvWarp0 = 11, kConvWarps = 4;
+constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
+constexpr int kRaw = 4;         // stages of codes
+constexpr int kScaleSlots = 8;  // tiles of scales, fetched four at a time
+constexpr int kSlots = 160;     // partial records of the workspace (a CTA of a split unit each)
+constexpr int kHeader = 256;
+constexpr float kRescale = 8.f;  // growth (log2) of a row's maximum before O is rescaled
+constexpr float kShift = 7.f;    // weights are held at 2^kShift of the reference
+
+struct PreArgs {
+    const __nv_bfloat16 *q;
+    const uint8_t *k_scales, *v_scales;
+    const int32_t *query_start, *block_table, *seq_lens;
+    __nv_bfloat16 *out;
+    float *partials;
+    uint32_t *counters;
+    int32_t *status;
+    int32_t batch, n_q, n_k, n_v, tokens, t_max, max_blocks;
+    int32_t page_size, page_shift, num_pages, sb, sub_rows, sub_shift;
+    int32_t splits;
+    long long scale_blocks;
+    float scale_log2;
+    uint64_t wait_limit_ns;
+};
+
+__device__ __forceinline__ int div_page(const PreArgs &a, int x) {
+    return a.page_shift >= 0 ? x >> a.page_shift : x / a.page_size;
+}
+__device__ __forceinline__ int clamp_to(int v, int hi) { return min(max(v, 0), hi); }
+
+// Rows of request b: first row of q and their number, both inside [0, tokens].
+__device__ __forceinline__ int2 request_rows(const PreArgs &a, int b) {
+    const int s = clamp_to(__ldg(a.query_start + b), a.tokens), e = clamp_to(__ldg(a.query_start + b + 1), a.tokens);
+    return make_int2(s, max(0, e - s));
+}
+
+template <int DK, int DV>
+struct Cfg {
+    static constexpr int Q_BYTES = BM * DK * 2;       // one query tile
+    static constexpr int RAW_K = BN * DK, RAW_V = BN * DV, RAW = RAW_K + RAW_V;
+    static constexpr int K_BYTES = 2 * RAW_K, V_BYTES = 2 * RAW_V, CONV = K_BYTES + V_BYTES;
+    static constexpr int STAGES = DK == 64 ? 3 : 2;   // converted tiles
+    static constexpr int OFF_CONV = QT * Q_BYTES;
+    static constexpr int OFF_RAW = OFF_CONV + STAGES * CONV;
+    static constexpr int OFF_MISC = OFF_RAW + kRaw * RAW;
+};
+
+struct Misc {
+    uint64_t raw_full[kRaw], raw_empty[kRaw], cv_full[3], cv_empty[3], sc_full[kScaleSlots], sc_empty[kScaleSlots];
+    uint64_t q_full, s_full[QT][2], p_full[QT], pv_done[QT], mma_done;
+    uint32_t k_mul[kScaleSlots][BN], v_mul[kScaleSlots][BN];  // 2^(e - e_ref) as f16 pairs, 0 behind the sequence
+    int k_ref[kScaleSlots], v_ref[kScaleSlots];               // e_ref
+    int ref[3][2];                                            // the same by converted stage: K, V
+    int found[8];                                             // unit: b, block, q row, rows, length; total blocks
+    uint32_t tmem_slot;
+    int abort_flag, last_flag;
+};
+
+constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t m) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(m));
+    return r;
+}
+
+// Sixteen codes -> sixteen f16 values times m, as two 16-byte chunks.
+__device__ __forceinline__ void widen16(const uint4 &c, uint32_t m, uint4 &lo, uint4 &hi) {
+    lo.x = mul_f16x2(e4m3x2_to_f16x2(c.x & 0xffffu), m);
+    lo.y = mul_f16x2(e4m3x2_to_f16x2(c.x >> 16), m);
+    lo.z = mul_f16x2(e4m3x2_to_f16x2(c.y & 0xffffu), m);
+    lo.w = mul_f16x2(e4m3x2_to_f16x2(c.y >> 16), m);
+    hi.x = mul_f16x2(e4m3x2_to_f16x2(c.z & 0xffffu), m);
+    hi.y = mul_f16x2(e4m3x2_to_f16x2(c.z >> 16), m);
+    hi.z = mul_f16x2(e4m3x2_to_f16x2(c.w & 0xffffu), m);
+    hi.w = mul_f16x2(e4m3x2_to_f16x2(c.w >> 16), m);
+}
+
+// Codes [64][D] -> f16 in 64-wide blocks [64 rows][128 bytes] with the 128-byte swizzle, by kConvWarps warps.
+template <int D>
+__device__ __forceinline__ void convert_side(const uint8_t *raw, uint8_t *dst, const uint32_t *mul, int tid) {
+    constexpr int LPR = D / 16;  // 16-code pieces of a row
+    static_assert(BN * LPR % (32 * kConvWarps) == 0, "whole rounds");
+#pragma unroll
+    for (int i = 0; i < BN * LPR / (32 * kConvWarps); ++i) {
+        const int at = tid + i * 32 * kConvWarps;
+        const int row = at / LPR, piece = at % LPR;
+        const uint32_t m = mul[row];
+        const uint4 c = lds128(raw + at * 16);
+        uint4 lo, hi;
+        widen16(c, m, lo, hi);
+        if (m == 0u) lo = hi = make_uint4(0, 0, 0, 0);  // behind the sequence: whatever is there may be NaN
+        const int chunk = piece * 2 & 7;
+        uint8_t *r = dst + (piece >> 2) * (BN * 128) + row * 128;
+        // the two blocks of a 128-wide row lie in the same banks: the second half's lanes store their chunks the other way round
+        const bool swap = piece >= 4;
+        *reinterpret_cast<uint4 *>(r + ((chunk + (swap ? 1 : 0)) ^ (row & 7)) * 16) = swap ? hi : lo;
+        *reinterpret_cast<uint4 *>(r + ((chunk + (swap ? 0 : 1)) ^ (row & 7)) * 16) = swap ? lo : hi;
+    }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kv8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const PreArgs a) {
+    using C = Cfg<DK, DV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    Misc &ms = *reinterpret_cast<Misc *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = &ms.abort_flag;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    const int h = blockIdx.x % a.n_q;
+
+    // ---- the unit: 256-row blocks of all requests, the last (longest context) first
+    if (warp == 0) {
+        int total = 0;
+        for (int pass = 0; pass < 2; ++pass) {
+            const int want = total - 1 - (int)(blockIdx.x / a.n_q);  // (second pass)
+            int acc = 0;
+            if (pass == 1 && lane == 0) ms.found[0] = -1;
+            __syncwarp();
+            for (int base = 0; base < a.batch; base += 32) {
+                const int b = base + lane;
+                int2 r = make_int2(0, 0);
+                if (b < a.batch) {
+                    r = request_rows(a, b);
+                    if (pass == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
+                        const int raw_s = __ldg(a.query_start + b), raw_e = __ldg(a.query_start + b + 1);
+                        const int T = __ldg(a.seq_lens + b);
+                        if (raw_s < 0 || raw_e < raw_s || raw_e > a.tokens || T < 0 || T > a.t_max || r.y > T)
+                            record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
+                    }
+                }
+                const int n = (r.y + kRows - 1) / kRows;
+                int incl = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += y;
+                }
+                const int before = acc + incl - n;
+                if (pass == 1 && n > 0 && want >= before && want < before + n) {
+                    ms.found[0] = b;
+                    ms.found[1] = want - before;
+                    ms.found[2] = r.x;
+                    ms.found[3] = r.y;
+                    ms.found[4] = clamp_to(__ldg(a.seq_lens + b), a.t_max);
+                }
+                acc += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (pass == 0) total = acc;
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    const int b = ms.found[0];
+    if (b < 0) return;
+    const int row0 = ms.found[1] * kRows, n_rows = ms.found[3], T = ms.found[4];
+    const int first = T - n_rows;  // position of the request's first row
+    const int q0 = ms.found[2] + row0;
+    const int kh = h / (a.n_q / a.n_k), vh = h / (a.n_q / a.n_v);
+
+    int n_kv[QT];  // K/V tiles that a query tile's rows see
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int rows = min(n_rows - row0 - t * BM, BM);
+        const int last = first + row0 + t * BM + rows - 1;
+        n_kv[t] = uniform(rows > 0 && last >= 0 ? last / BN + 1 : 0);
+    }
+    const int n_all = max(n_kv[0], n_kv[1]);
+    const int chunk = (n_all + a.splits - 1) / a.splits;
+    const int n0 = blockIdx.y * chunk, n1 = min(n_all, n0 + chunk);
+    if (n_all == 0 || n0 >= n1) {
+        if (n_all == 0 && blockIdx.y == 0)  // rows without a position
+            for (int e = tid; e < min(n_rows - row0, kRows) * (DV / 8); e += kThreads)
+                *reinterpret_cast<uint4 *>(a.out + ((size_t)(q0 + e / (DV / 8)) * a.n_q + h) * DV + e % (DV / 8) * 8) =
+                    make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int end[QT] = {min(n_kv[0], n1), min(n_kv[1], n1)};
+
+    if (tid == 0) {
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(&ms.raw_full[s], 1);
+            mbar_init(&ms.raw_empty[s], kConvWarps);
+        }
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(&ms.cv_full[s], kConvWarps);
+            mbar_init(&ms.cv_empty[s], 1);
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            mbar_init(&ms.sc_full[s], 1);
+            mbar_init(&ms.sc_empty[s], kConvWarps);
+        }
+        mbar_init(&ms.q_full, kSoftmaxWarps);
+        for (int t = 0; t < QT; ++t) {
+            mbar_init(&ms.s_full[t][0], 1);
+            mbar_init(&ms.s_full[t][1], 1);
+            mbar_init(&ms.p_full[t], 4);
+            mbar_init(&ms.pv_done[t], 1);
+        }
+        mbar_init(&ms.mma_done, 1);
+        ms.abort_flag = 0;
+        ms.last_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ms.tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)uniform((int)ms.tmem_slot);
+    constexpr uint32_t T_O = QT * 2 * BN;  // S_0 | S_0' | S_1 | S_1' | O_0 | O_1
+
+    if (warp == kLoadWarp) {
+        // ======================= TMA producer: codes, in sub-boxes inside one page (lane f holds sub-box f's page)
+        if (lane == 0) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+        }
+        auto subs = [&](int n) {
+            const int v = min(BN, T - n * BN) + a.sub_rows - 1;
+            return a.sub_shift >= 0 ? v >> a.sub_shift : v / a.sub_rows;
+        };
+        auto entry = [&](int n) {
+            return lane < subs(n)
+                       ? __ldg(a.block_table + (size_t)b * a.max_blocks + div_page(a, n * BN + lane * a.sub_rows))
+                       : 0;
+        };
+        int next = entry(n0), issued = 0, st = 0;
+        uint32_t par = 0;
+        for (int n = n0; n < n1; ++n) {
+            int page = next;
+            if (page < 0 || page >= a.num_pages) {
+                record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+                page = 0;
+            }
+            const int cnt = uniform(subs(n)), p = n * BN + lane * a.sub_rows;
+            const int row = p - div_page(a, p) * a.page_size;
+            if (n + 1 < n1) next = entry(n + 1);
+            if (issued >= kRaw) mbar_wait_bounded(&ms.raw_empty[st], par ^ 1u, a.wait_limit_ns, abort_flag, a.status);
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (elect_one()) mbar_arrive_expect_tx(&ms.raw_full[st], (uint32_t)(cnt * a.sub_rows * (DK + DV)));
+            __syncwarp();
+            uint8_t *kd = smem + C::OFF_RAW + st * C::RAW, *vd = kd + C::RAW_K;
+#pragma unroll 2
+            for (int f = 0; f < cnt; ++f) {
+                const int row_f = __shfl_sync(0xffffffffu, row, f), page_f = __shfl_sync(0xffffffffu, page, f);
+                if (elect_one()) {
+                    tma_load_4d(kd + f * a.sub_rows * DK, &tm_k, &ms.raw_full[st], 0, kh, row_f, page_f);
+                    tma_load_4d(vd + f * a.sub_rows * DV, &tm_v, &ms.raw_full[st], 0, vh, row_f, page_f);
+                }
+            }
+            __syncwarp();
+            ++issued;
+            if (++st == kRaw) {
+                st = 0;
+                par ^= 1u;
+            }
+        }
+        for (int k = max(0, issued - kRaw); k < issued; ++k)  // drain
+            mbar_wait_bounded(&ms.raw_full[k % kRaw], (uint32_t)(k / kRaw & 1), a.wait_limit_ns, nullptr, a.status);
+    } else if (warp == kScaleWarp) {
+        // ======================= scales, four tiles at a time: lane l looks after positions 2 l and 2 l + 1 of a tile
+        const int per_page = a.page_size / a.sb;
+        int v_run = kKv8MinExp;
+        for (int n = n0; n < n1; n += 4) {
+            int ek[4][2], ev[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int p = min((n + i) * BN + 2 * lane + e, T - 1);
+                    const int lp = div_page(a, p);
+                    int page = __ldg(a.block_table + (size_t)b * a.max_blocks + lp);
+                    if (page < 0 || page >= a.num_pages) page = 0;
+                    long long blk = (long long)page * per_page + (p - lp * a.page_size) / a.sb;
+                    if (!in_bounds(blk, a.scale_blocks, a.status)) blk = 0;
+                    ek[i][e] = __ldg(a.k_scales + blk * a.n_k + kh);
+                    ev[i][e] = __ldg(a.v_scales + blk * a.n_v + vh);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (n + i >= n1) break;
+                const int k = n + i - n0, slot = k % kScaleSlots;
+                if (k >= kScaleSlots)
+                    mbar_wait_bounded(&ms.sc_empty[slot], (uint32_t)((k / kScaleSlots - 1) & 1), a.wait_limit_ns, abort_flag,
+                                      a.status);
+                const int k0 = kv8_exp(ek[i][0]), k1 = kv8_exp(ek[i][1]), v0 = kv8_exp(ev[i][0]), v1 = kv8_exp(ev[i][1]);
+                const int kr = __reduce_max_sync(0xffffffffu, max(k0, k1));
+                const int vr = max(v_run, __reduce_max_sync(0xffffffffu, max(v0, v1)));
+                v_run = vr;
+                // 2^d in f16 for both halves of a word (2^-24 is its least; 0 is kept for positions behind the end)
+                auto mul = [&](int e, int ref, int pos) -> uint32_t {
+                    if (pos >= T) return 0u;
+                    const int d = max(e - ref, -24);
+                    const uint32_t hbits = d >= -14 ? (uint32_t)(d + 15) << 10 : 1u << (d + 24);
+                    return hbits * 0x10001u;
+                };
+                const int p = (n + i) * BN + 2 * lane;
+                ms.k_mul[slot][2 * lane] = mul(k0, kr, p);
+                ms.k_mul[slot][2 * lane + 1] = mul(k1, kr, p + 1);
+                ms.v_mul[slot][2 * lane] = mul(v0, vr, p);
+                ms.v_mul[slot][2 * lane + 1] = mul(v1, vr, p + 1);
+                if (lane == 0) {
+                    ms.k_ref[slot] = kr;
+                    ms.v_ref[slot] = vr;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.sc_full[slot]);
+            }
+        }
+    } else if (warp >= kConvWarp0) {
+        // ======================= codes -> f16
+        const int ct = tid - kConvWarp0 * 32;
+        int rs = 0, cs = 0;
+        uint32_t rp = 0, cp = 0;
+        for (int k = 0; k < n1 - n0; ++k) {
+            const int slot = k % kScaleSlots;
+            mbar_wait_bounded(&ms.sc_full[slot], (uint32_t)(k / kScaleSlots & 1), a.wait_limit_ns, abort_flag, a.status);
+            mbar_wait_bounded(&ms.raw_full[rs], rp, a.wait_limit_ns, abort_flag, a.status);
+            if (k >= C::STAGES) mbar_wait_bounded(&ms.cv_empty[cs], cp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
+            const uint8_t *raw = smem + C::OFF_RAW + rs * C::RAW;
+            uint8_t *dst = smem + C::OFF_CONV + cs * C::CONV;
+            convert_side<DK>(raw, dst, ms.k_mul[slot], ct);
+            convert_side<DV>(raw + C::RAW_K, dst + C::K_BYTES, ms.v_mul[slot], ct);
+            if (ct == 0) {
+                ms.ref[cs][0] = ms.k_ref[slot];
+                ms.ref[cs][1] = ms.v_ref[slot];
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ms.cv_full[cs]);
+                mbar_arrive(&ms.raw_empty[rs]);
+                mbar_arrive(&ms.sc_empty[slot]);
+            }
+            if (++rs == kRaw) {
+                rs = 0;
+                rp ^= 1u;
+            }
+            if (++cs == C::STAGES) {
+                cs = 0;
+                cp ^= 1u;
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ======================= MMA issue
+        constexpr uint32_t idesc_qk = idesc_f16(BM, BN, false), idesc_pv = idesc_f16(BM, DV, true);
+        const uint64_t q_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + C::OFF_CONV), 16, 1024);
+        const uint64_t v_desc = smem_desc_sw128(smem_addr(smem + C::OFF_CONV + C::K_BYTES), BN * 128, 1024);
+        mbar_wait_bounded(&ms.q_full, 0, a.wait_limit_ns, abort_flag, a.status);
+        tc_fence_after();
+        int cs = 0, pst = 0;  // stage of tile n, of tile n - 1
+        uint32_t cp = 0;
+        for (int n = n0; n <= n1; ++n) {
+            const int k = n - n0;
+            if (n < n1) {
+                mbar_wait_bounded(&ms.cv_full[cs], cp, a.wait_limit_ns, abort_flag, a.status);
+                tc_fence_after();
+                const uint64_t kd = k_desc + (uint32_t)(cs * (C::CONV >> 4));
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    if (n >= end[t]) continue;
+                    // S buffer k & 1 held S and P of tile n - 2: its P.V was issued ahead of this
+                    const uint64_t qd = q_desc + (uint32_t)(t * (C::Q_BYTES >> 4));
+                    const uint32_t t_s = tmem + (uint32_t)(t * 2 * BN + (k & 1) * BN);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < DK / 16; ++ks)
+                            umma_bf16(t_s, qd + (ks >> 2) * (BM * 128 >> 4) + (ks & 3) * 2,
+                                      kd + (ks >> 2) * (BN * 128 >> 4) + (ks & 3) * 2, idesc_qk, ks > 0 ? 1u : 0u);
+                        umma_commit(&ms.s_full[t][k & 1]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (k >= 1) {
+                const uint64_t vd = v_desc + (uint32_t)(pst * (C::CONV >> 4));
+                const uint32_t onto = (uint32_t)(k > 1);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    if (n - 1 >= end[t]) continue;
+                    mbar_wait_bounded(&ms.p_full[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+                    tc_fence_after();
+                    const uint32_t t_p = tmem + (uint32_t)(t * 2 * BN + ((k - 1) & 1) * BN);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < BN / 16; ++ks)
+                            umma_bf16_tmem_a(tmem + T_O + (uint32_t)(t * DV), t_p + ks * 8, vd + ks * (16 * 128 >> 4),
+                                             idesc_pv, ks > 0 ? 1u : onto);
+                        umma_commit(&ms.pv_done[t]);
+                    }
+                    __syncwarp();
+                }
+                if (elect_one()) umma_commit(&ms.cv_empty[pst]);
+                __syncwarp();
+                if (++pst == C::STAGES) pst = 0;
+            }
+            if (++cs == C::STAGES) {
+                cs = 0;
+                cp ^= 1u;
+            }
+        }
+        if (elect_one()) umma_commit(&ms.mma_done);
+        __syncwarp();
+        mbar_wait_bounded(&ms.mma_done, 0, a.wait_limit_ns, nullptr, a.status);
+    } else {
+        // ======================= softmax: warps 4 t .. 4 t + 3 hold query tile t, thread r its row r (TMEM lane r)
+        const int t = warp >> 2, r = tid & (BM - 1);
+        const int rr = row0 + t * BM + r;      // row of the request
+        const int i = first + rr;              // its position
+        const bool live = rr < n_rows;
+        const size_t qrow = ((size_t)(q0 + t * BM + r) * a.n_q + h);
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_o = tmem + T_O + (uint32_t)(t * DV) + lane_base;
+        float sc_row;  // scale * log2(e) * 2^(the query's exponent)
+        {
+            // the row in f16, its largest element brought into [2^14, 2^15) by a power of two
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow * DK);
+            uint8_t *dst = smem + t * C::Q_BYTES + r * 128;
+            const bool have = live && in_bounds((long long)qrow, (long long)a.tokens * a.n_q, a.status);
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < DK / 8; ++c) {
+                const uint4 x = have ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+                m = __vmaxu2(__vmaxu2(m, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+            }
+            m = max(m & 0xffffu, m >> 16);
+            const int se = min(141 - (int)(m >> 7), 126);
+            const float f = exp2_int(se);
+#pragma unroll
+            for (int c = 0; c < DK / 8; ++c) {
+                const uint4 x = have ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                uint4 y;
+                y.x = pack_f16x2(bf16lo(x.x) * f, bf16hi(x.x) * f);
+                y.y = pack_f16x2(bf16lo(x.y) * f, bf16hi(x.y) * f);
+                y.z = pack_f16x2(bf16lo(x.z) * f, bf16hi(x.z) * f);
+                y.w = pack_f16x2(bf16lo(x.w) * f, bf16hi(x.w) * f);
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * (BM * 128) + ((c & 7) ^ (r & 7)) * 16) = y;
+            }
+            // a row with infinities or NaN has no scale: its scores become NaN
+            sc_row = m >= 0x7f80u ? __int_as_float(0x7fffffff) : a.scale_log2 * exp2_int(-se);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_full);
+        }
+        float m_used = -INFINITY;  // log2 maximum that O and l are relative to
+        float l = 0.f;             // sum of the weights, 2^7 included
+        int v_run = 0;             // V exponent that O is relative to
+        int cs = 0;
+        uint32_t cp = 0;
+        for (int n = n0; n < end[t]; ++n) {
+            const int k = n - n0;
+            const uint32_t t_s = tmem + (uint32_t)(t * 2 * BN + (k & 1) * BN) + lane_base;
+            mbar_wait_bounded(&ms.cv_full[cs], cp, a.wait_limit_ns, abort_flag, a.status);
+            const int k_ref = ms.ref[cs][0], v_ref = ms.ref[cs][1];
+            if (++cs == C::STAGES) {
+                cs = 0;
+                cp ^= 1u;
+            }
+            float sc = sc_row * exp2_int(k_ref);
+            if (sc < 0x1p-126f) sc = 0x1p-126f;  // (a zero would turn masked scores into NaN)
+            mbar_wait_bounded(&ms.s_full[t][k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
+            tc_fence_after();
+            float s[BN];
+            {
+                uint32_t r0[32], r1[32];
+                tmem_ld32(t_s, r0);
+                tmem_ld32(t_s + 32, r1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    s[c] = __uint_as_float(r0[c]);
+                    s[32 + c] = __uint_as_float(r1[c]);
+                }
+            }
+            const int j0 = n * BN;
+            if (j0 + BN - 1 > first + row0 + t * BM) {  // causal mask, on tiles that reach past the tile's first row
+#pragma unroll
+                for (int c = 0; c < BN; ++c)
+                    if (j0 + c > i) s[c] = -INFINITY;
+            }
+            float mx8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(s[e], s[8 + e]);
+#pragma unroll
+            for (int c = 16; c < BN; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx8[e] = fmax3f(mx8[e], s[c + e], s[c + 8 + e]);
+            const float mx = fmax3f(fmax3f(mx8[0], mx8[1], mx8[2]), fmax3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+            const float m_new = mx * sc;
+            bool waited_pv = false;
+            if (k == 0) {
+                m_used = m_new == -INFINITY ? 0.f : m_new;
+                v_run = v_ref;
+            } else {
+                const bool grow = m_new > m_used + kRescale;
+                const bool v_grow = v_ref > v_run;  // the same in the whole tile
+                if (__any_sync(0xffffffffu, grow || v_grow)) {
+                    mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+                    waited_pv = true;
+                    tc_fence_after();
+                    const float lf = grow ? fast_exp2(m_used - m_new) : 1.f;
+                    const float alpha = v_grow ? lf * fast_exp2((float)(v_run - v_ref)) : lf;
+#pragma unroll 1
+                    for (int c = 0; c < DV; c += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(t_o + c, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+                        tmem_st32(t_o + c, x);
+                    }
+                    tmem_wait_st();
+                    if (grow) {
+                        l *= lf;
+                        m_used = m_new;
+                    }
+                    if (v_grow) v_run = v_ref;
+                }
+            }
+            // weights 2^(s - m + 7)
+            const f32x2_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(kShift - m_used, kShift - m_used);
+            uint32_t pk[BN / 2];
+            f32x2_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+                float t0, t1;
+                f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nm2), t0, t1);
+                const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                l2[(c >> 1) & 3] = f2_add(l2[(c >> 1) & 3], f2_pack(p0, p1));
+                pk[c >> 1] = pack_f16x2(p0, p1);
+            }
+            float la, lb;
+            f2_unpack(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])), la, lb);
+            l += la + lb;
+            tmem_st32(t_s, pk);
+            tmem_wait_st();
+            // at most one P.V behind, so that every phase of pv_done is waited for in turn
+            if (k >= 1 && !waited_pv)
+                mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.p_full[t]);
+        }
+        const int done = end[t] - n0;
+        if (done > 0) {
+            mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((done - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+            tc_fence_after();
+        }
+        const float o_scale = exp2f((float)v_run);  // (l carries the weights' 2^7 as O does)
+        if (a.splits == 1) {
+            const float inv_l = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row without a position: zeros)
+            __nv_bfloat16 *orow = a.out + qrow * DV;
+            const bool put = live && in_bounds((long long)qrow, (long long)a.tokens * a.n_q, a.status);
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 32) {
+                uint32_t x[32];
+                if (done > 0) {
+                    tmem_ld32(t_o + c, x);
+                    tmem_wait_ld();
+                }
+                if (put) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float y[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            y[j] = done > 0 && i >= 0 ? __uint_as_float(x[e + j]) * inv_l * o_scale : 0.f;
+                        *reinterpret_cast<uint4 *>(orow + c + e) =
+                            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                       pack_bf16x2(y[6], y[7]));
+                    }
+                }
+            }
+        } else {
+            // this split's partial: m, l and O relative to m, the record's rows in a row of d_v + 2 columns
+            float *rec = a.partials + ((size_t)(blockIdx.x * a.splits + blockIdx.y) * kRows + t * BM + r) * (DV + 2);
+            const bool some = done > 0 && i >= 0 && n0 * BN <= i;  // the row sees a position of this split
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 32) {
+                uint32_t x[32];
+                if (done > 0) {
+                    tmem_ld32(t_o + c, x);
+                    tmem_wait_ld();
+                }
+                if (live)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        __stcg(reinterpret_cast<float2 *>(rec + c + e),
+                               some ? make_float2(__uint_as_float(x[e]) * o_scale, __uint_as_float(x[e + 1]) * o_scale)
+                                    : make_float2(0.f, 0.f));
+            }
+            if (live) __stcg(reinterpret_cast<float2 *>(rec + DV), some ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f));
+            __threadfence();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (a.splits == 1) return;
+
+    // ---- split units: the last CTA merges the partials
+    const int used = (n_all + chunk - 1) / chunk;
+    if (tid == 0) {
+        __threadfence();
+        ms.last_flag = atomicAdd(a.counters + blockIdx.x, 1u) == (unsigned)(used - 1);
+    }
+    __syncthreads();
+    if (!*(volatile int *)&ms.last_flag) return;
+    __threadfence();
+    const int rows = min(n_rows - row0, kRows);
+    for (int e = tid; e < rows * (DV / 2); e += kThreads) {
+        const int r = e / (DV / 2), d = e % (DV / 2) * 2;
+        const float *base = a.partials + ((size_t)blockIdx.x * a.splits * kRows + r) * (DV + 2);
+        const size_t step = (size_t)kRows * (DV + 2);
+        float M = -INFINITY;
+        for (int s = 0; s < used; ++s) M = fmaxf(M, __ldcg(base + s * step + DV));
+        float L = 0.f, x = 0.f, y = 0.f;
+        for (int s = 0; s < used; ++s) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(base + s * step + DV));
+            if (ml.x == -INFINITY) continue;  // nothing of this split is seen by the row
+            const float2 o = __ldcg(reinterpret_cast<const float2 *>(base + s * step + d));
+            const float f = fast_exp2(ml.x - M);
+            L = fmaf(f, ml.y, L);
+            x = fmaf(f, o.x, x);
+            y = fmaf(f, o.y, y);
+        }
+        const float inv = M == -INFINITY ? 0.f : 1.f / L;
+        *reinterpret_cast<uint32_t *>(a.out + ((size_t)(q0 + r) * a.n_q + h) * DV + d) = pack_bf16x2(x * inv, y * inv);
+    }
+    if (tid == 0) a.counters[blockIdx.x] = 0u;
+}
+
+// ------------------------------------------------------------------ host side
+
+using PreFn = void (*)(CUtensorMap, CUtensorMap, PreArgs);
+
+template <int DK, int DV>
+PreFn plan(int *smem) {
+    *smem = Cfg<DK, DV>::OFF_MISC + (int)sizeof(Misc) + 1024;
+    static_assert(Cfg<DK, DV>::OFF_MISC + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory");
+    return prefill_kv8_kernel<DK, DV>;
+}
+
+size_t prefill_kv8_workspace_size(const diffqkv_dims_t *d) {
+    if (validate_dims(d) != DIFFQKV_OK) return 0;
+    return kHeader + kSlots * sizeof(uint32_t) + 256 + (size_t)kSlots * kRows * (d->d_v + 2) * sizeof(float);
+}
+
+diffqkv_status_t prefill_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cache_t *cache, const void *q,
+                                    const int32_t *query_start, int32_t tokens, const int32_t *block_table,
+                                    int32_t max_blocks, const int32_t *seq_lens, void *out, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+    diffqkv_status_t st = validate_kv8(d, cache);
+    if (st != DIFFQKV_OK) return st;
+    if (!q || !query_start || !block_table || !seq_lens || !out || max_blocks < 1 || tokens < 1)
+        return DIFFQKV_ERR_INVALID_ARG;
+    const int P = cache->page_size;
+    if ((long long)max_blocks * P > 0x7fffffffLL) return DIFFQKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(query_start) & 3u))
+        return DIFFQKV_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < prefill_kv8_workspace_size(d)) return DIFFQKV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DIFFQKV_ERR_MISALIGNED;
+    // blocks of kRows rows over all requests: at most this many
+    const long long units = ((long long)tokens / kRows + d->batch) * d->n_q;
+    if (units > 0x7fffffffLL) return DIFFQKV_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    st = current_device_info(&dev);
+    if (st != DIFFQKV_OK) return st;
+
+    PreArgs a;
+    a.sub_rows = std::gcd(BN, P);
+    auto log2_or_minus1 = [](int v) {
+        if (v & (v - 1)) return -1;
+        int l = 0;
+        while ((1 << l) < v) ++l;
+        return l;
+    };
+    a.sub_shift = log2_or_minus1(a.sub_rows);
+    a.page_size = P;
+    a.page_shift = log2_or_minus1(P);
+    CUtensorMap tm_k, tm_v;
+    auto map = [&](CUtensorMap *m, const void *base, int dim, int heads) {
+        const uint64_t dims[4] = {(uint64_t)dim, (uint64_t)heads, (uint64_t)P, (uint64_t)cache->num_pages};
+        const uint64_t strides[3] = {(uint64_t)dim, (uint64_t)dim * heads, (uint64_t)dim * heads * P};
+        const uint32_t box[4] = {(uint32_t)dim, 1, (uint32_t)a.sub_rows, 1};
+        return make_tensor_map_u8(m, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    };
+    st = map(&tm_k, cache->k_pages, d->d_k, d->n_k);
+    if (st == DIFFQKV_OK) st = map(&tm_v, cache->v_pages, d->d_v, d->n_v);
+    if (st != DIFFQKV_OK) return st;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.query_start = query_start;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.status = reinterpret_cast<int32_t *>(ws);
+    a.counters = reinterpret_cast<uint32_t *>(ws + kHeader);
+    a.partials = reinterpret_cast<float *>(ws + (kHeader + kSlots * sizeof(uint32_t) + 255) / 256 * 256);
+    a.batch = d->batch;
+    a.n_q = d->n_q;
+    a.n_k = d->n_k;
+    a.n_v = d->n_v;
+    a.tokens = tokens;
+    a.t_max = max_blocks * P;
+    a.max_blocks = max_blocks;
+    a.num_pages = cache->num_pages;
+    a.sb = cache->scale_block;
+    a.scale_blocks = (long long)cache->num_pages * (P / cache->scale_block);
+    a.scale_log2 = (float)((double)d->scale * 1.4426950408889634);
+    a.wait_limit_ns = kWaitLimitNs;
+    // units for fewer than half of the SMs: cut their K/V tiles
+    a.splits = units * 2 <= dev.num_sms ? (int)(std::min(dev.num_sms, kSlots) / units) : 1;
+    int smem = 0;
+    PreFn fn = d->d_k == 64 ? (d->d_v == 64 ? plan<64, 64>(&smem) : plan<64, 128>(&smem))
+                            : (d->d_v == 64 ? plan<128, 64>(&smem) : plan<128, 128>(&smem));
+    if (ensure_dynamic_smem((const void *)fn, smem) != DIFFQKV_OK) return DIFFQKV_ERR_CUDA;
+    fn<<<dim3((unsigned)units, (unsigned)a.splits), kThreads, smem, stream>>>(tm_k, tm_v, a);
+    return cudaGetLastError() == cudaSuccess ? DIFFQKV_OK : DIFFQKV_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace diffqkv
+
+extern "C" size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims) {
+    return diffqkv::prefill_kv8_workspace_size(dims);
+}
+
+extern "C" diffqkv_status_t diffqkv_prefill_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
+                                                      const void *q, const int32_t *query_start, int32_t tokens,
+                                                      const int32_t *block_table, int32_t max_blocks,
+                                                      const int32_t *seq_lens, void *out, void *workspace,
+                                                      size_t workspace_bytes, diffqkv_stream_t stream) {
+    diffqkv::ApiRange nvtx_range("diffqkv_prefill_paged_kv8");
+    return diffqkv::prefill_kv8_launch(dims, cache, q, query_start, tokens, block_table, max_blocks, seq_lens, out,
+                                       workspace, workspace_bytes, (cudaStream_t)stream);
+}

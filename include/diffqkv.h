@@ -575,6 +575,38 @@ diffqkv_status_t diffqkv_decode_paged_kv8(const diffqkv_dims_t *dims, const diff
                                           const int32_t *seq_lens, int32_t max_seq_len, void *out, void *workspace,
                                           size_t workspace_bytes, diffqkv_stream_t stream);
 
+/* Bytes of workspace diffqkv_prefill_paged_kv8 needs (0 if dims are invalid); zero-filled
+ * before its first use, and left reusable by every call that completes, as diffqkv_decode's. */
+size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
+
+/*
+ * Causal attention of a ragged batch of query rows over an 8-bit paged cache (prompts,
+ * chunks of prompts over a cached prefix, or a few rows to verify).
+ *
+ *   q           [tokens, n_q, d_k]      bf16; request b owns rows query_start[b] ..
+ *                                       query_start[b + 1] - 1 (n_b of them, 0 allowed)
+ *   query_start [B + 1] int32           as diffqkv_page_map writes it
+ *   block_table [B, max_blocks] int32   as in diffqkv_decode_paged_kv8
+ *   seq_lens    [B] int32               positions of the sequence, the n_b new ones included
+ *                                       (stored beforehand, diffqkv_kv8_store)
+ *   out         [tokens, n_q, d_v]      bf16; rows behind query_start[B] are not written
+ *
+ * Row r of request b sits at position seq_lens[b] - n_b + r and attends to positions 0 up
+ * to its own.  Lengths outside [0, max_blocks * page_size], starts outside [0, tokens] or
+ * descending, and n_b > seq_lens[b] are clamped and flagged DIFFQKV_ERR_DEVICE_SEQLEN in the
+ * workspace's error word; a row without a position gets zeros.  Bad table entries as in
+ * diffqkv_prefill_causal_paged.  Codes and queries are converted to f16 with power-of-two
+ * scales (exactly, but for blocks whose scale is 2^15 below the largest of their tile of 64 positions,
+ * for K, or of the sequence so far, for V), products are summed in fp32, and softmax weights are rounded
+ * to f16 for the second product.  A NaN in a stored V row can also reach rows up to 255 before it.
+ * tokens >= 1.  workspace as above.
+ */
+diffqkv_status_t diffqkv_prefill_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
+                                           const void *q, const int32_t *query_start, int32_t tokens,
+                                           const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                           void *out, void *workspace, size_t workspace_bytes,
+                                           diffqkv_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Device error word                                                        */
 /* ------------------------------------------------------------------------ */

@@ -95,3 +95,39 @@ def check_decode(out, q, p, table, lens, scale, what=""):
     assert np.isfinite(got).all(), what
     over = np.abs(got - ref) - tol
     assert over.max(initial=-1.0) <= 0, f"{what}: {over.max()} over at {np.unravel_index(over.argmax(), over.shape)}"
+
+
+def check_prefill(out, q, start, p, table, lens, scale, what=""):
+    """Prefill rows [tokens, n_q, d_v] against the fp64 formula on the pools ``p``: row r of request b (rows start[b] ..
+    start[b + 1] - 1) sits at position lens[b] - n_b + r.
+
+    Tolerance: the bf16 rounding, 2^-8 |out|; f16 weights, 2^-11 of each (and 2^-31 of the largest, absolutely), as
+    much again for fp32 sums and the exponentials: 2^-10 * sum_j p_j |v_j| + positions * 2^-31 p_max max|v|; V rows in f16
+    below the range its exponent reference leaves: 2^-25 of the largest exponent; a score's error as in
+    :func:`attention_tolerance`."""
+    k, v = dequant(p)
+    n_q = q.shape[1]
+    n_k, n_v = k.shape[2], v.shape[2]
+    got = out.double().cpu().numpy()
+    kg, vg = oracle.gather_paged(k, table, lens).double(), oracle.gather_paged(v, table, lens).double()
+    for b, n in enumerate(int(t) for t in lens):
+        rows = int(start[b + 1]) - int(start[b])
+        if rows == 0:
+            continue
+        pos = torch.arange(n - rows, n)
+        held = table[b, :-(-n // v.shape[1])].long()
+        e = kv8.exponents(p[3][held]).max(axis=(0, 1), initial=-120)
+        for h in range(n_q):
+            qh = q[start[b]:start[b + 1], h].double()
+            kh, vh = kg[b, :n, h // (n_q // n_k)], vg[b, :n, h // (n_q // n_v)]
+            s = (qh @ kh.T * scale).masked_fill(torch.arange(n)[None] > pos[:, None], float("-inf"))
+            w = torch.softmax(s, 1)
+            ref, mag = w @ vh, w @ vh.abs()
+            smag = ((qh.abs() @ kh.abs().T) * scale).masked_fill(torch.isinf(s), 0).amax(1, keepdim=True)
+            top = 2.0 ** float(e[h // (n_q // n_v)])
+            tol = (2 ** -8 + 2 ** -16) * ref.abs() + (2 ** -10 + 2 ** -14.9 * smag) * mag + 2 ** -25 * top + \
+                (pos + 1)[:, None] * 2.0 ** -31 * w.amax(1, keepdim=True) * 448 * top
+            g = torch.from_numpy(got[start[b]:start[b + 1], h])
+            assert torch.isfinite(g).all(), f"{what} request {b} head {h}"
+            over = ((g - ref).abs() - tol).max().item()
+            assert over <= 0, f"{what} request {b} head {h}: {over} over"
