@@ -394,17 +394,29 @@ def prefill_causal_paged(q, k_pages, v_pages, block_table, prefix_len: int, *, s
     return out
 
 
-def _cuda(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> ctypes.c_void_p:
-    """Address of a contiguous tensor of the given type and shape on the current device."""
+def _refuse(t, name, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
+
+
+def _addr(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of the given type and shape on device ``dev``.  (These checks are most of a
+    short call's time on the host: one expression where all is well, the reasons looked up only to refuse.)"""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape)
+
+
+def _stream_on(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """The given stream's handle, or that of the current stream of ``dev``, which must be the current device."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, not on the current CUDA device")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -425,6 +437,9 @@ def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     max_blocks = block_table.shape[1]
+    dev = seq_lens.get_device()
+    if dev < 0:
+        raise ValueError("seq_lens must be a CUDA tensor")
     if slot_map is None:
         if capacity is None:
             raise ValueError("give slot_map, or capacity")
@@ -441,13 +456,13 @@ def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
     if status is not None:
         _status_word(status)
     st = lib().diffqkv_page_map(
-        B, _cuda(seq_lens, "seq_lens", i32, (B,)), _cuda(new_lens, "new_lens", i32, (B,)),
-        _cuda(block_table, "block_table", i32, (B, max_blocks)), max_blocks, page_size, num_pages,
-        _cuda(free_pages, "free_pages", i32, (free_pages.numel(),)), free_pages.numel(), cap,
-        _cuda(query_start, "query_start", i32, (B + 1,)), _cuda(slot_map, "slot_map", i32, (cap,)),
-        None if positions is None else _cuda(positions, "positions", i32, (cap,)),
-        _cuda(total_lens, "total_lens", i32, (B,)), _cuda(pages_used, "pages_used", i32, (1,)), _ptr(status),
-        _stream_ptr(stream))
+        B, _addr(seq_lens, "seq_lens", i32, (B,), dev), _addr(new_lens, "new_lens", i32, (B,), dev),
+        _addr(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks, page_size, num_pages,
+        _addr(free_pages, "free_pages", i32, (free_pages.numel(),), dev), free_pages.numel(), cap,
+        _addr(query_start, "query_start", i32, (B + 1,), dev), _addr(slot_map, "slot_map", i32, (cap,), dev),
+        None if positions is None else _addr(positions, "positions", i32, (cap,), dev),
+        _addr(total_lens, "total_lens", i32, (B,), dev), _addr(pages_used, "pages_used", i32, (1,), dev),
+        None if status is None else status.data_ptr(), _stream_on(dev, stream))
     check(st, "diffqkv_page_map")
     return query_start, slot_map, positions, total_lens, pages_used
 
@@ -467,7 +482,7 @@ def kv8_pools(num_pages: int, page_size: int, n_k: int, n_v: int, d_k: int, d_v:
 
 
 def _kv8_cache(k_pages, v_pages, k_scales, v_scales):
-    """The C struct of an 8-bit cache, and (n_k, n_v, d_k, d_v)."""
+    """The C struct of an 8-bit cache, its device, and n_k, n_v, d_k, d_v."""
     if k_pages.dim() != 4 or v_pages.dim() != 4 or k_scales.dim() != 3:
         raise ValueError("k_pages / v_pages must be [num_pages, page_size, heads, d] and the scales "
                          "[num_pages, page_size // scale_block, heads]")
@@ -476,12 +491,16 @@ def _kv8_cache(k_pages, v_pages, k_scales, v_scales):
     parts = k_scales.shape[1]
     if parts < 1 or page_size % parts:
         raise ValueError("the scale blocks of k_scales do not divide the page")
+    dev = k_pages.get_device()
+    if dev < 0:
+        raise ValueError("k_pages must be a CUDA tensor")
     e4m3, u8 = torch.float8_e4m3fn, torch.uint8
     cache = _capi.Kv8Cache(
-        _cuda(k_pages, "k_pages", e4m3, k_pages.shape), _cuda(v_pages, "v_pages", e4m3, (num_pages, page_size, n_v, d_v)),
-        _cuda(k_scales, "k_scales", u8, (num_pages, parts, n_k)), _cuda(v_scales, "v_scales", u8, (num_pages, parts, n_v)),
-        num_pages, page_size, page_size // parts)
-    return cache, (n_k, n_v, d_k, d_v)
+        _addr(k_pages, "k_pages", e4m3, k_pages.shape, dev),
+        _addr(v_pages, "v_pages", e4m3, (num_pages, page_size, n_v, d_v), dev),
+        _addr(k_scales, "k_scales", u8, (num_pages, parts, n_k), dev),
+        _addr(v_scales, "v_scales", u8, (num_pages, parts, n_v), dev), num_pages, page_size, page_size // parts)
+    return cache, dev, n_k, n_v, d_k, d_v
 
 
 def kv8_store(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, k_pages: torch.Tensor,
@@ -491,15 +510,15 @@ def kv8_store(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, 
     (int32 [T], page * page_size + row, negative: skipped) names: e4m3 codes with a power-of-two scale for each block
     of positions and head, grown when a later row needs it (``diffqkv_kv8_store``).  The tokens of a scale block must
     be consecutive, as :func:`page_map` lays them out."""
-    cache, (n_k, n_v, d_k, d_v) = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
+    cache, dev, n_k, n_v, d_k, d_v = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
     T = slot_map.numel()
     if status is not None:
         _status_word(status)
     dims = Dims(1, n_k * n_v, n_k, n_v, d_k, d_v, 1.0)
     st = lib().diffqkv_kv8_store(
-        dims, cache, _cuda(k_new, "k_new", torch.bfloat16, (T, n_k, d_k)),
-        _cuda(v_new, "v_new", torch.bfloat16, (T, n_v, d_v)), _cuda(slot_map, "slot_map", torch.int32, (T,)), T,
-        _ptr(status), _stream_ptr(stream))
+        dims, cache, _addr(k_new, "k_new", torch.bfloat16, (T, n_k, d_k), dev),
+        _addr(v_new, "v_new", torch.bfloat16, (T, n_v, d_v), dev), _addr(slot_map, "slot_map", torch.int32, (T,), dev), T,
+        None if status is None else status.data_ptr(), _stream_on(dev, stream))
     check(st, "diffqkv_kv8_store")
 
 
@@ -511,7 +530,7 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     """:func:`decode` over an 8-bit paged cache: e4m3 pools k_pages [num_pages, page_size, n_k, d_k] and v_pages
     [num_pages, page_size, n_v, d_v], scale bytes [num_pages, page_size // scale_block, heads], block_table int32
     [B, max_blocks], seq_lens int32 [B].  Returns bf16 [B, n_q, d_v]."""
-    cache, (n_k, n_v, d_k, d_v) = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
+    cache, dev, n_k, n_v, d_k, d_v = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [B, n_q, d_k] and block_table [B, max_blocks]")
     B, n_q, _ = q.shape
@@ -523,10 +542,11 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     if workspace is None:
         workspace = decode_workspace(dims, device=q.device)
     st = lib().diffqkv_decode_paged_kv8(
-        dims, cache, _cuda(q, "q", bf16, (B, n_q, d_k)), _cuda(block_table, "block_table", torch.int32, (B, max_blocks)),
-        max_blocks, _cuda(seq_lens, "seq_lens", torch.int32, (B,)), 0 if max_seq_len is None else max_seq_len,
-        _cuda(out, "out", bf16, (B, n_q, d_v)), _cuda(workspace, "workspace", torch.uint8, workspace.shape),
-        workspace.numel(), _stream_ptr(stream))
+        dims, cache, _addr(q, "q", bf16, (B, n_q, d_k), dev),
+        _addr(block_table, "block_table", torch.int32, (B, max_blocks), dev), max_blocks,
+        _addr(seq_lens, "seq_lens", torch.int32, (B,), dev), 0 if max_seq_len is None else max_seq_len,
+        _addr(out, "out", bf16, (B, n_q, d_v), dev), _addr(workspace, "workspace", torch.uint8, workspace.shape, dev),
+        workspace.numel(), _stream_on(dev, stream))
     check(st, "diffqkv_decode_paged_kv8")
     return out
 
@@ -548,7 +568,7 @@ def prefill_paged_kv8(q: torch.Tensor, query_start: torch.Tensor, k_pages: torch
     owning rows query_start[b] .. query_start[b + 1] - 1 (int32 [B + 1], as :func:`page_map` writes it) at the last
     positions of its seq_lens[b] (int32 [B], the new rows included and stored).  Returns bf16 [tokens, n_q, d_v]; rows
     behind query_start[B] are not written."""
-    cache, (n_k, n_v, d_k, d_v) = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
+    cache, dev, n_k, n_v, d_k, d_v = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [tokens, n_q, d_k] and block_table [B, max_blocks]")
     T, n_q, _ = q.shape
@@ -560,10 +580,10 @@ def prefill_paged_kv8(q: torch.Tensor, query_start: torch.Tensor, k_pages: torch
     if workspace is None:
         workspace = prefill_paged_kv8_workspace(dims, q.device)
     st = lib().diffqkv_prefill_paged_kv8(
-        dims, cache, _cuda(q, "q", bf16, (T, n_q, d_k)), _cuda(query_start, "query_start", i32, (B + 1,)), T,
-        _cuda(block_table, "block_table", i32, (B, max_blocks)), max_blocks, _cuda(seq_lens, "seq_lens", i32, (B,)),
-        _cuda(out, "out", bf16, (T, n_q, d_v)), _cuda(workspace, "workspace", torch.uint8, workspace.shape),
-        workspace.numel(), _stream_ptr(stream))
+        dims, cache, _addr(q, "q", bf16, (T, n_q, d_k), dev), _addr(query_start, "query_start", i32, (B + 1,), dev), T,
+        _addr(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks,
+        _addr(seq_lens, "seq_lens", i32, (B,), dev), _addr(out, "out", bf16, (T, n_q, d_v), dev),
+        _addr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(), _stream_on(dev, stream))
     check(st, "diffqkv_prefill_paged_kv8")
     return out
 
