@@ -34,8 +34,8 @@ namespace {
 
 constexpr int BM = 128, QT = 2, BN = 64;
 constexpr int kRows = QT * BM;
-constexpr int kSoftmaxWarps = 4 * QT;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kConvWarp0 = 11, kConvWarps = 4;
+constexpr int kSoftmaxWarps = 8 * QT;  // two warps per 32 rows, 32 columns of S each
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kScaleWarp = 18, kConvWarp0 = 19, kConvWarps = 4;
 constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kRaw = 4;         // stages of codes
 constexpr int kScaleSlots = 8;  // tiles of scales, fetched four at a time
@@ -88,6 +88,7 @@ struct Misc {
     uint32_t k_mul[kScaleSlots][BN], v_mul[kScaleSlots][BN];  // 2^(e - e_ref) as f16 pairs, 0 behind the sequence
     int k_ref[kScaleSlots], v_ref[kScaleSlots];               // e_ref
     int ref[3][2];                                            // the same by converted stage: K, V
+    float row_s[QT][2][BM];                                   // exchange between the two halves of a row
     int found[8];                                             // unit: b, block, q row, rows, length; total blocks
     uint32_t tmem_slot;
     int abort_flag, last_flag;
@@ -119,27 +120,62 @@ __device__ __forceinline__ void widen16(const uint4 &c, uint32_t m, uint4 &lo, u
     hi.w = mul_f16x2(e4m3x2_to_f16x2(c.w >> 16), m);
 }
 
-// Codes [64][D] -> f16 in 64-wide blocks [64 rows][128 bytes] with the 128-byte swizzle, by kConvWarps warps.
+// Codes [64][D] -> f16 in 64-wide blocks [64 rows][128 bytes] with the 128-byte swizzle, by kConvWarps warps: a thread has
+// the same 16 columns of every kStep-th row, so that its addresses are one base and constant steps.
 template <int D>
-__device__ __forceinline__ void convert_side(const uint8_t *raw, uint8_t *dst, const uint32_t *mul, int tid) {
-    constexpr int LPR = D / 16;  // 16-code pieces of a row
-    static_assert(BN * LPR % (32 * kConvWarps) == 0, "whole rounds");
-#pragma unroll
-    for (int i = 0; i < BN * LPR / (32 * kConvWarps); ++i) {
-        const int at = tid + i * 32 * kConvWarps;
-        const int row = at / LPR, piece = at % LPR;
-        const uint32_t m = mul[row];
-        const uint4 c = lds128(raw + at * 16);
-        uint4 lo, hi;
-        widen16(c, m, lo, hi);
-        if (m == 0u) lo = hi = make_uint4(0, 0, 0, 0);  // behind the sequence: whatever is there may be NaN
-        const int chunk = piece * 2 & 7;
-        uint8_t *r = dst + (piece >> 2) * (BN * 128) + row * 128;
-        // the two blocks of a 128-wide row lie in the same banks: the second half's lanes store their chunks the other way round
-        const bool swap = piece >= 4;
-        *reinterpret_cast<uint4 *>(r + ((chunk + (swap ? 1 : 0)) ^ (row & 7)) * 16) = swap ? hi : lo;
-        *reinterpret_cast<uint4 *>(r + ((chunk + (swap ? 0 : 1)) ^ (row & 7)) * 16) = swap ? lo : hi;
+struct Widen {
+    static constexpr int LPR = D / 16;                       // 16-code pieces of a row
+    static constexpr int kStep = 32 * kConvWarps / LPR;      // rows between a thread's pieces: a multiple of 8
+    static constexpr int kRounds = BN / kStep;
+    static_assert(kStep % 8 == 0 && BN % kStep == 0, "swizzle phase of a thread");
+    uint32_t src, dst0, dst1, row;
+    bool swap;
+    __device__ explicit Widen(int tid) {
+        const int piece = tid % LPR, chunk = piece * 2 & 7;
+        row = tid / LPR;
+        src = tid * 16;
+        // the two blocks of a 128-wide row lie in the same banks: the second half's threads store their two chunks the
+        // other way round
+        swap = piece >= 4;
+        const uint32_t at = (piece >> 2) * (BN * 128) + row * 128;
+        dst0 = at + ((chunk + (swap ? 1 : 0)) ^ (row & 7)) * 16;
+        dst1 = at + ((chunk + (swap ? 0 : 1)) ^ (row & 7)) * 16;
     }
+    __device__ __forceinline__ void run(const uint8_t *raw, uint8_t *out, const uint32_t *mul, bool tail) const {
+        uint4 c[kRounds];
+        uint32_t m[kRounds];
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            c[i] = lds128(raw + src + i * (kStep * D));
+            m[i] = mul[row + i * kStep];
+        }
+        if (tail) {  // behind the sequence: whatever is there may be NaN
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i)
+                if (m[i] == 0u) c[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            uint4 lo, hi;
+            widen16(c[i], m[i], lo, hi);
+            *reinterpret_cast<uint4 *>(out + dst0 + i * (kStep * 128)) = swap ? hi : lo;
+            *reinterpret_cast<uint4 *>(out + dst1 + i * (kStep * 128)) = swap ? lo : hi;
+        }
+    }
+};
+
+// Barrier of the two warps of `id`; true where the predicate holds in any of their threads.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
 }
 
 template <int DK, int DV>
@@ -239,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < QT; ++t) {
             mbar_init(&ms.s_full[t][0], 1);
             mbar_init(&ms.s_full[t][1], 1);
-            mbar_init(&ms.p_full[t], 4);
+            mbar_init(&ms.p_full[t], 8);
             mbar_init(&ms.pv_done[t], 1);
         }
         mbar_init(&ms.mma_done, 1);
@@ -358,6 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kConvWarp0) {
         // ======================= codes -> f16
         const int ct = tid - kConvWarp0 * 32;
+        const Widen<DK> widen_k(ct);
+        const Widen<DV> widen_v(ct);
         int rs = 0, cs = 0;
         uint32_t rp = 0, cp = 0;
         for (int k = 0; k < n1 - n0; ++k) {
@@ -367,8 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k >= C::STAGES) mbar_wait_bounded(&ms.cv_empty[cs], cp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
             const uint8_t *raw = smem + C::OFF_RAW + rs * C::RAW;
             uint8_t *dst = smem + C::OFF_CONV + cs * C::CONV;
-            convert_side<DK>(raw, dst, ms.k_mul[slot], ct);
-            convert_side<DV>(raw + C::RAW_K, dst + C::K_BYTES, ms.v_mul[slot], ct);
+            const bool tail = (n0 + k + 1) * BN > T;
+            widen_k.run(raw, dst, ms.k_mul[slot], tail);
+            widen_v.run(raw + C::RAW_K, dst + C::K_BYTES, ms.v_mul[slot], tail);
             if (ct == 0) {
                 ms.ref[cs][0] = ms.k_ref[slot];
                 ms.ref[cs][1] = ms.v_ref[slot];
@@ -452,14 +491,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait_bounded(&ms.mma_done, 0, a.wait_limit_ns, nullptr, a.status);
     } else {
-        // ======================= softmax: warps 4 t .. 4 t + 3 hold query tile t, thread r its row r (TMEM lane r)
-        const int t = warp >> 2, r = tid & (BM - 1);
-        const int rr = row0 + t * BM + r;      // row of the request
-        const int i = first + rr;              // its position
+        // ======================= softmax: warps 8 t .. 8 t + 7 hold query tile t; a row (TMEM lane r) belongs to two threads,
+        // one for each half of a tile's columns.  Four warps a scheduler hide one another's latencies.
+        const int t = warp >> 3, half = warp >> 2 & 1, r = (warp & 3) * 32 + lane;
+        const int bar = 1 + t * 4 + (warp & 3);  // named barrier of the two warps that share rows
+        const int rr = row0 + t * BM + r;        // row of the request
+        const int i = first + rr;                // its position
         const bool live = rr < n_rows;
         const size_t qrow = ((size_t)(q0 + t * BM + r) * a.n_q + h);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_o = tmem + T_O + (uint32_t)(t * DV) + lane_base;
+        constexpr int HV = DV / 2;               // this thread's columns of O
+        const uint32_t t_o = tmem + T_O + (uint32_t)(t * DV + half * HV) + lane_base;
         float sc_row;  // scale * log2(e) * 2^(the query's exponent)
         {
             // the row in f16, its largest element brought into [2^14, 2^15) by a power of two
@@ -477,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int se = min(141 - (int)(m >> 7), 126);
             const float f = exp2_int(se);
 #pragma unroll
-            for (int c = 0; c < DK / 8; ++c) {
+            for (int c0 = 0; c0 < DK / 16; ++c0) {
+                const int c = half * (DK / 16) + c0;
                 const uint4 x = have ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
                 uint4 y;
                 y.x = pack_f16x2(bf16lo(x.x) * f, bf16hi(x.x) * f);
@@ -492,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.q_full);
         }
-        float m_used = -INFINITY;  // log2 maximum that O and l are relative to
-        float l = 0.f;             // sum of the weights, 2^7 included
-        int v_run = 0;             // V exponent that O is relative to
+        float m_used = 0.f;  // log2 maximum that O and l are relative to (the same in both halves)
+        float l = 0.f;       // this half's sum of the weights, 2^7 included
+        int v_run = 0;       // V exponent that O is relative to
         int cs = 0;
         uint32_t cp = 0;
         for (int n = n0; n < end[t]; ++n) {
@@ -510,54 +553,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (sc < 0x1p-126f) sc = 0x1p-126f;  // (a zero would turn masked scores into NaN)
             mbar_wait_bounded(&ms.s_full[t][k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
-            float s[BN];
-            {
-                uint32_t r0[32], r1[32];
-                tmem_ld32(t_s, r0);
-                tmem_ld32(t_s + 32, r1);
-                tmem_wait_ld();
+            uint32_t x[32];
+            tmem_ld32(t_s + (uint32_t)(half * 32), x);
+            tmem_wait_ld();
+            const int j0 = n * BN + half * 32;
+            if (j0 + 31 > first + row0 + t * BM) {  // causal mask, on columns that reach past the tile's first row
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    s[c] = __uint_as_float(r0[c]);
-                    s[32 + c] = __uint_as_float(r1[c]);
-                }
+                for (int e = 0; e < 32; ++e)
+                    if (j0 + e > i) x[e] = 0xff800000u;
             }
-            const int j0 = n * BN;
-            if (j0 + BN - 1 > first + row0 + t * BM) {  // causal mask, on tiles that reach past the tile's first row
+            auto sv = [&](int e) { return __uint_as_float(x[e]); };
+            float m4[4];
 #pragma unroll
-                for (int c = 0; c < BN; ++c)
-                    if (j0 + c > i) s[c] = -INFINITY;
-            }
-            float mx8[8];
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(sv(e), sv(4 + e));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(s[e], s[8 + e]);
+            for (int e = 8; e < 32; e += 8)
 #pragma unroll
-            for (int c = 16; c < BN; c += 16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mx8[e] = fmax3f(mx8[e], s[c + e], s[c + 8 + e]);
-            const float mx = fmax3f(fmax3f(mx8[0], mx8[1], mx8[2]), fmax3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-            const float m_new = mx * sc;
-            bool waited_pv = false;
-            if (k == 0) {
-                m_used = m_new == -INFINITY ? 0.f : m_new;
-                v_run = v_ref;
-            } else {
-                const bool grow = m_new > m_used + kRescale;
-                const bool v_grow = v_ref > v_run;  // the same in the whole tile
-                if (__any_sync(0xffffffffu, grow || v_grow)) {
+                for (int c = 0; c < 4; ++c) m4[c] = fmax3f(m4[c], sv(e + c), sv(e + 4 + c));
+            const float m_half = fmaxf(fmax3f(m4[0], m4[1], m4[2]), m4[3]) * sc;
+            // Both halves have read S behind this barrier (P goes over columns of the other half), and agree on whether a
+            // reference has to move: the first tile, a row that grew by 2^8, a larger V exponent
+            const bool v_grow = v_ref > v_run;
+            if (pair_any(bar, k == 0 || v_grow || m_half > m_used + kRescale)) {
+                ms.row_s[t][half][r] = m_half;
+                named_barrier(bar, 64);
+                const float m_new = fmaxf(m_half, ms.row_s[t][1 - half][r]);
+                named_barrier(bar, 64);
+                if (k == 0) {
+                    m_used = m_new == -INFINITY ? 0.f : m_new;
+                    v_run = v_ref;
+                } else {
                     mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
-                    waited_pv = true;
                     tc_fence_after();
+                    const bool grow = m_new > m_used + kRescale;
                     const float lf = grow ? fast_exp2(m_used - m_new) : 1.f;
                     const float alpha = v_grow ? lf * fast_exp2((float)(v_run - v_ref)) : lf;
 #pragma unroll 1
-                    for (int c = 0; c < DV; c += 32) {
-                        uint32_t x[32];
-                        tmem_ld32(t_o + c, x);
+                    for (int c = 0; c < HV; c += 16) {
+                        uint32_t y[16];
+                        tmem_ld_cols<16>(t_o + c, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-                        tmem_st32(t_o + c, x);
+                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                        tmem_st_cols<16>(t_o + c, y);
                     }
                     tmem_wait_st();
                     if (grow) {
@@ -569,24 +607,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // weights 2^(s - m + 7)
             const f32x2_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(kShift - m_used, kShift - m_used);
-            uint32_t pk[BN / 2];
-            f32x2_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+            uint32_t pk[16];
+            f32x2_t l2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < BN; c += 2) {
+            for (int e = 0; e < 32; e += 2) {
                 float t0, t1;
-                f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nm2), t0, t1);
+                f2_unpack(f2_fma(f2_pack(sv(e), sv(e + 1)), sc2, nm2), t0, t1);
                 const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
-                l2[(c >> 1) & 3] = f2_add(l2[(c >> 1) & 3], f2_pack(p0, p1));
-                pk[c >> 1] = pack_f16x2(p0, p1);
+                l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(p0, p1));
+                pk[e >> 1] = pack_f16x2(p0, p1);
             }
+            tmem_st_cols<16>(t_s + (uint32_t)(half * 16), pk);
             float la, lb;
-            f2_unpack(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])), la, lb);
+            f2_unpack(f2_add(l2[0], l2[1]), la, lb);
             l += la + lb;
-            tmem_st32(t_s, pk);
             tmem_wait_st();
             // at most one P.V behind, so that every phase of pv_done is waited for in turn
-            if (k >= 1 && !waited_pv)
-                mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+            if (k >= 1) mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.p_full[t]);
@@ -596,28 +633,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((done - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
         }
+        ms.row_s[t][half][r] = l;
+        named_barrier(bar, 64);
+        l += ms.row_s[t][1 - half][r];
         const float o_scale = exp2f((float)v_run);  // (l carries the weights' 2^7 as O does)
         if (a.splits == 1) {
             const float inv_l = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row without a position: zeros)
-            __nv_bfloat16 *orow = a.out + qrow * DV;
+            __nv_bfloat16 *orow = a.out + qrow * DV + half * HV;
             const bool put = live && in_bounds((long long)qrow, (long long)a.tokens * a.n_q, a.status);
 #pragma unroll 1
-            for (int c = 0; c < DV; c += 32) {
-                uint32_t x[32];
+            for (int c = 0; c < HV; c += 16) {
+                uint32_t y[16];
                 if (done > 0) {
-                    tmem_ld32(t_o + c, x);
+                    tmem_ld_cols<16>(t_o + c, y);
                     tmem_wait_ld();
                 }
                 if (put) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float y[8];
+                    for (int e = 0; e < 16; e += 8) {
+                        float z[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            y[j] = done > 0 && i >= 0 ? __uint_as_float(x[e + j]) * inv_l * o_scale : 0.f;
+                            z[j] = done > 0 && i >= 0 ? __uint_as_float(y[e + j]) * inv_l * o_scale : 0.f;
                         *reinterpret_cast<uint4 *>(orow + c + e) =
-                            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                       pack_bf16x2(y[6], y[7]));
+                            make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                                       pack_bf16x2(z[6], z[7]));
                     }
                 }
             }
@@ -626,20 +666,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *rec = a.partials + ((size_t)(blockIdx.x * a.splits + blockIdx.y) * kRows + t * BM + r) * (DV + 2);
             const bool some = done > 0 && i >= 0 && n0 * BN <= i;  // the row sees a position of this split
 #pragma unroll 1
-            for (int c = 0; c < DV; c += 32) {
-                uint32_t x[32];
+            for (int c = 0; c < HV; c += 16) {
+                uint32_t y[16];
                 if (done > 0) {
-                    tmem_ld32(t_o + c, x);
+                    tmem_ld_cols<16>(t_o + c, y);
                     tmem_wait_ld();
                 }
                 if (live)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        __stcg(reinterpret_cast<float2 *>(rec + c + e),
-                               some ? make_float2(__uint_as_float(x[e]) * o_scale, __uint_as_float(x[e + 1]) * o_scale)
+                    for (int e = 0; e < 16; e += 2)
+                        __stcg(reinterpret_cast<float2 *>(rec + half * HV + c + e),
+                               some ? make_float2(__uint_as_float(y[e]) * o_scale, __uint_as_float(y[e + 1]) * o_scale)
                                     : make_float2(0.f, 0.f));
             }
-            if (live) __stcg(reinterpret_cast<float2 *>(rec + DV), some ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f));
+            if (live && half == 0)
+                __stcg(reinterpret_cast<float2 *>(rec + DV), some ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f));
             __threadfence();
         }
     }
