@@ -13,13 +13,19 @@
 //   code = rn_e4m3(x * 2^-e)                  (infinities, and magnitudes above 448 * 2^119, become +-448; NaN stays NaN)
 // Rows above the written ones stay as they are.
 //
-// The call reads 2 bytes and writes 1 per element; with a prompt's rows that is what bounds it.  A run is
-// a maximal stretch of consecutive tokens in one block; one warp owns a (run, head), so the block's
-// maximum needs no atomics and no second launch: the warp keeps up to kVec 16-byte loads of the run's
-// rows in registers between the maximum and the rounding (a run of 32 rows of 64 or 16 of 128), and
-// reads longer runs twice (the second time out of L1 / L2).  The maximum is taken on the bf16 bit patterns
-// (two 16-bit maxima an instruction) and crosses the warp in one redux.
+// The call reads 2 bytes and writes 1 per element; with a prompt's rows that is what bounds it, with a decode step's
+// the launch and four dependent loads.  A run is a maximal stretch of consecutive tokens in one block.  One group of lanes
+// owns a (run, head), so the block's maximum needs no atomics and no second launch; the rows stay in registers between the
+// maximum and the rounding (longer runs are read twice).  The first rows are requested together with the slots,
+// before it is known which run they belong to: most often they are the ones.
+// Two shapes of group, by the rows a run can have:
+//  * blocks of more than kRowBlock positions, and steps of few tokens: `share` warps, as many as hold a whole block in
+//    registers (16 rows of 128 or 32 of 64 a warp), over the runs that begin in the CTA's chunk of tokens; the maximum crosses
+//    a warp in one redux and the warps through shared memory;
+//  * smaller blocks: the 8 or 16 lanes of one row, every (token, head) has a group and those whose token does not begin
+//    a run have nothing to do.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv8.cuh"
@@ -29,8 +35,10 @@ namespace diffqkv {
 namespace {
 
 constexpr int kStoreWarps = 8;
-constexpr int kVec = 8;        // 16-byte loads a lane keeps
-constexpr int kMaxTokens = 16; // tokens whose runs one CTA may lead
+constexpr int kRunVec = 8, kRowVec = 4;  // 16-byte loads a lane keeps, by shape of group
+constexpr int kMaxTokens = 32; // tokens whose runs one CTA may lead
+constexpr int kRowBlock = 4;   // blocks up to this size take a row's lanes
+constexpr int kFewTokens = 512;
 
 struct StoreArgs {
     const uint4 *k_new, *v_new;
@@ -40,6 +48,7 @@ struct StoreArgs {
     int32_t tokens, n_k, n_v, sb, sb_shift;  // sb_shift: log2(sb), or -1
     int32_t slots;                           // num_pages * page_size
     int32_t chunk;                           // tokens of one CTA
+    int32_t share;                           // warps of one (run, head)
 };
 
 __device__ __forceinline__ int block_of(const StoreArgs &a, int slot) {
@@ -84,57 +93,83 @@ __device__ __forceinline__ uint32_t move4(uint32_t codes, float f) {
     return e4m3x2(a * f, b * f) | (e4m3x2(c * f, d * f) << 16);
 }
 
-// One (run, head): the run's tokens t0 .. t0 + len - 1 lie in scale block `blk`, lowest row `low`.
-template <int D>
+// Largest of v over the group of G lanes.
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (G == 32) return __reduce_max_sync(0xffffffffu, v);
+    const uint32_t mask = ((1u << G) - 1u) << (threadIdx.x & 31 & ~(G - 1));
+#pragma unroll
+    for (int off = G / 2; off >= 1; off >>= 1) v = max(v, __shfl_xor_sync(mask, v, off));
+    return v;
+}
+
+// One (run, head): the run's tokens t0 .. t0 + len - 1 lie in scale block `blk`, lowest row `low`.  `lane`: of the group.
+// keep: the lane's first rows of the run if `kept`.  `share` groups (warps) split the rows, this one being `mine`; their
+// maxima meet in `cross` (shared memory, one word a warp of the CTA) at a named barrier of theirs.
+template <int D, int G, int VEC>
 __device__ __forceinline__ void store_run(const StoreArgs &a, const uint4 *x, uint8_t *pages, uint8_t *scales,
-                                          int heads, int head, int t0, int len, int blk, int low, int lane) {
-    constexpr int LPR = D / 8;      // lanes of a row (8 elements each)
-    constexpr int ROWS = 32 / LPR;  // rows of one warp-wide load
-    const int sub = lane / LPR, part = lane % LPR;
+                                          int heads, int head, int t0, int len, int blk, int low, int lane,
+                                          uint4 (&keep)[VEC], bool kept, int share = 1, int mine = 0,
+                                          uint32_t *cross = nullptr) {
+    constexpr int LPR = D / 8;              // lanes of a row (8 elements each)
+    const int ROWS = G / LPR * share;       // rows of one load of the groups
+    const int sub = mine * (G / LPR) + lane / LPR, part = lane % LPR;
     uint8_t *byte = scales + (size_t)blk * heads + head;
     const int old = low > 0 ? kv8_exp(*byte) : 0;
     auto row_of = [&](int i) { return x + ((size_t)(t0 + i) * heads + head) * LPR + part; };
 
-    uint4 keep[kVec];
     uint32_t m = 0;
-    for (int base = 0; base < len; base += ROWS * kVec) {
+    for (int base = sub; base < len; base += ROWS * VEC) {
+        if (!kept || base != sub)
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const int i = base + v * ROWS + sub;
-            keep[v] = i < len ? __ldg(row_of(i)) : make_uint4(0, 0, 0, 0);
-        }
+            for (int v = 0; v < VEC; ++v) {
+                const int i = base + v * ROWS;
+                if (i < len) keep[v] = __ldg(row_of(i));
+            }
 #pragma unroll
-        for (int v = 0; v < kVec; ++v)
-            m = max_bits(max_bits(max_bits(max_bits(m, keep[v].x), keep[v].y), keep[v].z), keep[v].w);
+        for (int v = 0; v < VEC; ++v)
+            if (base + v * ROWS < len)
+                m = max_bits(max_bits(max_bits(max_bits(m, keep[v].x), keep[v].y), keep[v].z), keep[v].w);
     }
-    uint32_t amax = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    auto all_max = [&](uint32_t v) {
+        v = group_max<G>(v);
+        if (share > 1) {
+            const int first = ((int)threadIdx.x >> 5) - mine;
+            named_barrier(1 + first / share, share * 32);
+            if (lane == 0) cross[first + mine] = v;
+            named_barrier(1 + first / share, share * 32);
+            for (int w = 0; w < share; ++w) v = max(v, cross[first + w]);
+        }
+        return v;
+    };
+    uint32_t amax = all_max(max(m & 0xffffu, m >> 16));
     if (amax >= 0x7f80u) {  // an infinity or NaN among them: the maximum again without those
         m = 0;
         for (int i = sub; i < len; i += ROWS) {
             const uint4 r = __ldg(row_of(i));
             m = max_finite_bits(max_finite_bits(max_finite_bits(max_finite_bits(m, r.x), r.y), r.z), r.w);
         }
-        amax = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        amax = all_max(max(m & 0xffffu, m >> 16));
     }
     int e = scale_exp(amax);
     if (low > 0) e = max(e, old);
     const float f = exp2_int(-e);
 
-    for (int base = 0; base < len; base += ROWS * kVec) {
-        if (len > ROWS * kVec) {
+    for (int base = sub; base < len; base += ROWS * VEC) {
+        int slot[VEC];
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                const int i = base + v * ROWS + sub;
-                if (i < len) keep[v] = __ldg(row_of(i));
+        for (int v = 0; v < VEC; ++v) {
+            const int i = base + v * ROWS;
+            if (i < len) {
+                if (len > ROWS * VEC) keep[v] = __ldg(row_of(i));
+                slot[v] = __ldg(a.slot_map + t0 + i);  // (inside the pool: it belongs to the run)
             }
         }
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const int i = base + v * ROWS + sub;
-            if (i >= len) continue;
-            const int slot = slot_of(a, t0 + i);
-            *reinterpret_cast<uint2 *>(pages + ((size_t)slot * heads + head) * D + part * 8) = quantise8(keep[v], f);
-        }
+        for (int v = 0; v < VEC; ++v)
+            if (base + v * ROWS < len)
+                *reinterpret_cast<uint2 *>(pages + ((size_t)slot[v] * heads + head) * D + part * 8) =
+                    quantise8(keep[v], f);
     }
     if (low > 0 && e > old) {
         const float g = exp2_int(max(old - e, -126));  // 2^-126 already takes every code to zero
@@ -146,37 +181,46 @@ __device__ __forceinline__ void store_run(const StoreArgs &a, const uint4 *x, ui
             *p = c;
         }
     }
-    if (lane == 0 && (low == 0 || e != old)) *byte = (uint8_t)(e + 127);
+    if (lane == 0 && mine == 0 && (low == 0 || e != old)) *byte = (uint8_t)(e + 127);
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kStoreWarps * 32) kv8_store_kernel(const StoreArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int warp = (threadIdx.x >> 5) + kStoreWarps * blockIdx.y;
-    const int warps = kStoreWarps * gridDim.y;
+template <int DK, int DV, bool SHARED>
+__global__ void __launch_bounds__(kStoreWarps * 32, 3) kv8_store_runs_kernel(const StoreArgs a) {
+    __shared__ uint32_t cross[kStoreWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int share = SHARED ? a.share : 1;
     const int heads = a.n_k + a.n_v;
+    // the (run, head)s of this warp: one head, the runs that begin in the CTA's chunk of tokens
+    const int head = blockIdx.y * (kStoreWarps / share) + warp / share, mine = warp % share;
     const int t_begin = blockIdx.x * a.chunk;
+    uint4 keep[kRunVec];
+    if (!SHARED && head < heads) {  // the chunk's rows, before the slots are there
+        const bool k = head < a.n_k;
+        const int lpr = k ? DK / 8 : DV / 8, n = k ? a.n_k : a.n_v, rows = 32 / lpr;
+        const uint4 *x = (k ? a.k_new : a.v_new) + (size_t)(k ? head : head - a.n_k) * lpr + lane % lpr;
+#pragma unroll
+        for (int v = 0; v < kRunVec; ++v) {
+            const int i = v * rows + lane / lpr;
+            if (i < a.chunk && t_begin + i < a.tokens) keep[v] = __ldg(x + (size_t)(t_begin + i) * n * lpr);
+        }
+    }
     // every warp finds the runs its CTA leads: lane i looks at token t_begin + i
     const int t = t_begin + lane;
     int slot = -1, blk = -1;
     bool leads = false;
     if (lane < a.chunk && t < a.tokens) {
         const int raw = __ldg(a.slot_map + t);
-        if (raw >= a.slots && warp == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+        const int before = t > 0 ? slot_of(a, t - 1) : -1;
+        if (raw >= a.slots && warp == 0 && blockIdx.y == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
         slot = raw < a.slots ? raw : -1;
         if (slot >= 0) {
             blk = block_of(a, slot);
-            const int before = t > 0 ? slot_of(a, t - 1) : -1;
             leads = before < 0 || block_of(a, before) != blk;
         }
     }
-    int pair = warp;  // (run, head) pairs go round the warps
+    if (head >= heads) return;
     for (unsigned left = __ballot_sync(0xffffffffu, leads); left; left &= left - 1) {
         const int src = __ffs(left) - 1;
-        if (pair >= heads) {
-            pair -= heads;
-            continue;
-        }
         const int t0 = t_begin + src;
         const int run_blk = __shfl_sync(0xffffffffu, blk, src);
         // the run's length and lowest row, 32 tokens at a time
@@ -193,17 +237,68 @@ __global__ void __launch_bounds__(kStoreWarps * 32) kv8_store_kernel(const Store
                 open = false;
             }
         }
-        for (; pair < heads; pair += warps) {
-            if (pair < a.n_k)
-                store_run<DK>(a, a.k_new, a.k_pages, a.k_scales, a.n_k, pair, t0, len, run_blk, low, lane);
-            else
-                store_run<DV>(a, a.v_new, a.v_pages, a.v_scales, a.n_v, pair - a.n_k, t0, len, run_blk, low, lane);
-        }
-        pair -= heads;
+        const bool kept = !SHARED && src == 0 && len <= a.chunk;
+        if (head < a.n_k)
+            store_run<DK, 32>(a, a.k_new, a.k_pages, a.k_scales, a.n_k, head, t0, len, run_blk, low, lane, keep, kept, share,
+                              mine, cross);
+        else
+            store_run<DV, 32>(a, a.v_new, a.v_pages, a.v_scales, a.n_v, head - a.n_k, t0, len, run_blk, low, lane, keep, kept,
+                              share, mine, cross);
     }
 }
 
-using StoreFn = void (*)(StoreArgs);
+// One group of D / 8 lanes per (token, head); blockIdx.y: K or V.
+template <int D>
+__device__ __forceinline__ void store_rows(const StoreArgs &a, const uint4 *x, uint8_t *pages, uint8_t *scales, int heads,
+                                           bool flag) {
+    constexpr int LPR = D / 8;
+    const unsigned group = (blockIdx.x * (kStoreWarps * 32u) + threadIdx.x) / LPR;
+    const int t = (int)(group / (unsigned)heads), head = (int)(group - (unsigned)t * heads);
+    if (t >= a.tokens) return;
+    uint4 keep[kRowVec];
+    keep[0] = __ldg(x + (size_t)group * LPR + threadIdx.x % LPR);  // this row, before the slots are there
+    const int raw = __ldg(a.slot_map + t);
+    const int before = t > 0 ? slot_of(a, t - 1) : -1;
+    int next = t + 1 < a.tokens ? slot_of(a, t + 1) : -1;
+    if (raw >= a.slots && flag && head == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+    if (raw < 0 || raw >= a.slots) return;
+    const int blk = block_of(a, raw);
+    if (before >= 0 && block_of(a, before) == blk) return;
+    int len = 1, low = raw - blk * a.sb;
+    while (next >= 0 && block_of(a, next) == blk) {
+        low = min(low, next - blk * a.sb);
+        ++len;
+        next = t + len < a.tokens ? slot_of(a, t + len) : -1;
+    }
+#pragma unroll
+    for (int v = 1; v < kRowVec; ++v)
+        if (v < len) keep[v] = __ldg(x + ((size_t)(t + v) * heads + head) * LPR + threadIdx.x % LPR);
+    store_run<D, LPR>(a, x, pages, scales, heads, head, t, len, blk, low, (int)threadIdx.x % LPR, keep, true);
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kStoreWarps * 32) kv8_store_rows_kernel(const StoreArgs a) {
+    if (blockIdx.y == 0)
+        store_rows<DK>(a, a.k_new, a.k_pages, a.k_scales, a.n_k, true);
+    else
+        store_rows<DV>(a, a.v_new, a.v_pages, a.v_scales, a.n_v, false);
+}
+
+template <int DK, int DV>
+void store_launch(const StoreArgs &a, cudaStream_t stream) {
+    if (a.sb <= kRowBlock && a.tokens > kFewTokens) {
+        const long long k = (long long)a.tokens * a.n_k * (DK / 8), v = (long long)a.tokens * a.n_v * (DV / 8);
+        const long long ctas = (std::max(k, v) + kStoreWarps * 32 - 1) / (kStoreWarps * 32);
+        kv8_store_rows_kernel<DK, DV><<<dim3((unsigned)ctas, 2), kStoreWarps * 32, 0, stream>>>(a);
+        return;
+    }
+    const int per_cta = kStoreWarps / a.share;
+    const dim3 grid((a.tokens + a.chunk - 1) / a.chunk, (a.n_k + a.n_v + per_cta - 1) / per_cta);
+    if (a.share > 1)
+        kv8_store_runs_kernel<DK, DV, true><<<grid, kStoreWarps * 32, 0, stream>>>(a);
+    else
+        kv8_store_runs_kernel<DK, DV, false><<<grid, kStoreWarps * 32, 0, stream>>>(a);
+}
 
 diffqkv_status_t kv8_store_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cache_t *c, const void *k_new,
                                   const void *v_new, const int32_t *slot_map, int32_t tokens, int32_t *status,
@@ -237,16 +332,17 @@ diffqkv_status_t kv8_store_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cac
     if ((a.sb & (a.sb - 1)) == 0)
         for (a.sb_shift = 0; (1 << a.sb_shift) < a.sb;) ++a.sb_shift;
     a.slots = c->num_pages * c->page_size;
-    // few tokens: one CTA for each token and eight heads, so that every warp has one pair; many: the
-    // chunk covers a block's tokens and the warps go round its heads
-    const int heads = d->n_k + d->n_v;
-    a.chunk = std::min(kMaxTokens, std::max(1, tokens / (4 * dev.num_sms)));
-    const int gx = (tokens + a.chunk - 1) / a.chunk;
-    const int gy = (heads + kStoreWarps - 1) / kStoreWarps;
-    if (gy > 65535) return DIFFQKV_ERR_UNSUPPORTED;
-    StoreFn fn = d->d_k == 64 ? (d->d_v == 64 ? kv8_store_kernel<64, 64> : kv8_store_kernel<64, 128>)
-                              : (d->d_v == 64 ? kv8_store_kernel<128, 64> : kv8_store_kernel<128, 128>);
-    fn<<<dim3(gx, gy), kStoreWarps * 32, 0, stream>>>(a);
+    // a CTA's chunk is about a block of tokens, one token where there are few; the warps of a (run, head) hold a block
+    a.chunk = tokens <= kFewTokens ? 1 : std::min(kMaxTokens, std::max(16, a.sb));
+    a.share = 1;
+    if (tokens > kFewTokens)
+        while (a.share < kStoreWarps && a.share * 32 * kRunVec * 8 / std::max(d->d_k, d->d_v) < a.sb) a.share *= 2;
+    if ((d->n_k + d->n_v) > 65535) return DIFFQKV_ERR_UNSUPPORTED;
+    if ((long long)tokens * std::max(d->n_k, d->n_v) * 16 > 0x7fffffffLL) return DIFFQKV_ERR_UNSUPPORTED;  // thread index
+    if (d->d_k == 64)
+        d->d_v == 64 ? store_launch<64, 64>(a, stream) : store_launch<64, 128>(a, stream);
+    else
+        d->d_v == 64 ? store_launch<128, 64>(a, stream) : store_launch<128, 128>(a, stream);
     return cudaGetLastError() == cudaSuccess ? DIFFQKV_OK : DIFFQKV_ERR_CUDA;
 }
 
