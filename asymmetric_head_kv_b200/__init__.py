@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import _capi
-from ._capi import DiffqkvError, Dims, DecodePlan, DecodeTuning, check, lib
+from ._capi import DiffqkvError, Dims, DecodePlan, DecodeTuning, check, lib, serving
 
 __all__ = [
     "decode", "decode_workspace", "decode_plan", "decode_from_host", "decode_topv", "decode_topv_workspace",
@@ -394,31 +394,6 @@ def prefill_causal_paged(q, k_pages, v_pages, block_table, prefix_len: int, *, s
     return out
 
 
-def _refuse(t, name, dtype, shape):
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
-
-
-def _addr(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> int:
-    """Address of a contiguous tensor of the given type and shape on device ``dev``.  (These checks are most of a
-    short call's time on the host: one expression where all is well, the reasons looked up only to refuse.)"""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, name, dtype, shape)
-
-
-def _stream_on(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
-    """The given stream's handle, or that of the current stream of ``dev``, which must be the current device."""
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, not on the current CUDA device")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-
-
 def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
              page_size: int, num_pages: int, query_start: Optional[torch.Tensor] = None,
              slot_map: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
@@ -433,36 +408,20 @@ def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
     give them, or ``capacity`` (rows of the step's token buffer) to have them allocated.  A step that does not fit
     ``capacity`` or ``free_pages`` is dropped as a whole and flagged (``diffqkv_page_map``)."""
     i32 = torch.int32
-    B = seq_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    max_blocks = block_table.shape[1]
-    dev = seq_lens.get_device()
-    if dev < 0:
-        raise ValueError("seq_lens must be a CUDA tensor")
     if slot_map is None:
         if capacity is None:
             raise ValueError("give slot_map, or capacity")
         slot_map = torch.empty(int(capacity), dtype=i32, device=seq_lens.device)
         if positions is None:
             positions = torch.empty_like(slot_map)
-    cap = slot_map.numel()
     if query_start is None:
-        query_start = torch.empty(B + 1, dtype=i32, device=seq_lens.device)
+        query_start = torch.empty(seq_lens.numel() + 1, dtype=i32, device=seq_lens.device)
     if total_lens is None:
-        total_lens = torch.empty(B, dtype=i32, device=seq_lens.device)
+        total_lens = torch.empty(seq_lens.numel(), dtype=i32, device=seq_lens.device)
     if pages_used is None:
         pages_used = torch.empty(1, dtype=i32, device=seq_lens.device)
-    if status is not None:
-        _status_word(status)
-    st = lib().diffqkv_page_map(
-        B, _addr(seq_lens, "seq_lens", i32, (B,), dev), _addr(new_lens, "new_lens", i32, (B,), dev),
-        _addr(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks, page_size, num_pages,
-        _addr(free_pages, "free_pages", i32, (free_pages.numel(),), dev), free_pages.numel(), cap,
-        _addr(query_start, "query_start", i32, (B + 1,), dev), _addr(slot_map, "slot_map", i32, (cap,), dev),
-        None if positions is None else _addr(positions, "positions", i32, (cap,), dev),
-        _addr(total_lens, "total_lens", i32, (B,), dev), _addr(pages_used, "pages_used", i32, (1,), dev),
-        None if status is None else status.data_ptr(), _stream_on(dev, stream))
+    st = serving().page_map(seq_lens, new_lens, block_table, free_pages, page_size, num_pages, query_start, slot_map,
+                            positions, total_lens, pages_used, status, stream)
     check(st, "diffqkv_page_map")
     return query_start, slot_map, positions, total_lens, pages_used
 
@@ -481,28 +440,6 @@ def kv8_pools(num_pages: int, page_size: int, n_k: int, n_v: int, d_k: int, d_v:
     return tuple(out)
 
 
-def _kv8_cache(k_pages, v_pages, k_scales, v_scales):
-    """The C struct of an 8-bit cache, its device, and n_k, n_v, d_k, d_v."""
-    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_scales.dim() != 3:
-        raise ValueError("k_pages / v_pages must be [num_pages, page_size, heads, d] and the scales "
-                         "[num_pages, page_size // scale_block, heads]")
-    num_pages, page_size, n_k, d_k = k_pages.shape
-    n_v, d_v = v_pages.shape[2], v_pages.shape[3]
-    parts = k_scales.shape[1]
-    if parts < 1 or page_size % parts:
-        raise ValueError("the scale blocks of k_scales do not divide the page")
-    dev = k_pages.get_device()
-    if dev < 0:
-        raise ValueError("k_pages must be a CUDA tensor")
-    e4m3, u8 = torch.float8_e4m3fn, torch.uint8
-    cache = _capi.Kv8Cache(
-        _addr(k_pages, "k_pages", e4m3, k_pages.shape, dev),
-        _addr(v_pages, "v_pages", e4m3, (num_pages, page_size, n_v, d_v), dev),
-        _addr(k_scales, "k_scales", u8, (num_pages, parts, n_k), dev),
-        _addr(v_scales, "v_scales", u8, (num_pages, parts, n_v), dev), num_pages, page_size, page_size // parts)
-    return cache, dev, n_k, n_v, d_k, d_v
-
-
 def kv8_store(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, k_pages: torch.Tensor,
               v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, *,
               status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -510,16 +447,15 @@ def kv8_store(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, 
     (int32 [T], page * page_size + row, negative: skipped) names: e4m3 codes with a power-of-two scale for each block
     of positions and head, grown when a later row needs it (``diffqkv_kv8_store``).  The tokens of a scale block must
     be consecutive, as :func:`page_map` lays them out."""
-    cache, dev, n_k, n_v, d_k, d_v = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
-    T = slot_map.numel()
-    if status is not None:
-        _status_word(status)
-    dims = Dims(1, n_k * n_v, n_k, n_v, d_k, d_v, 1.0)
-    st = lib().diffqkv_kv8_store(
-        dims, cache, _addr(k_new, "k_new", torch.bfloat16, (T, n_k, d_k), dev),
-        _addr(v_new, "v_new", torch.bfloat16, (T, n_v, d_v), dev), _addr(slot_map, "slot_map", torch.int32, (T,), dev), T,
-        None if status is None else status.data_ptr(), _stream_on(dev, stream))
+    st = serving().kv8_store(k_new, v_new, slot_map, k_pages, v_pages, k_scales, v_scales, status, stream)
     check(st, "diffqkv_kv8_store")
+
+
+def _kv8_dims(q, batch: int, k_pages, v_pages) -> Dims:
+    """Dims of an attention over an 8-bit cache (for its workspace)."""
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("q must be 3-D and k_pages / v_pages [num_pages, page_size, heads, d]")
+    return Dims(batch, q.shape[1], k_pages.shape[2], v_pages.shape[2], k_pages.shape[3], v_pages.shape[3], 1.0)
 
 
 def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
@@ -530,23 +466,12 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     """:func:`decode` over an 8-bit paged cache: e4m3 pools k_pages [num_pages, page_size, n_k, d_k] and v_pages
     [num_pages, page_size, n_v, d_v], scale bytes [num_pages, page_size // scale_block, heads], block_table int32
     [B, max_blocks], seq_lens int32 [B].  Returns bf16 [B, n_q, d_v]."""
-    cache, dev, n_k, n_v, d_k, d_v = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be [B, n_q, d_k] and block_table [B, max_blocks]")
-    B, n_q, _ = q.shape
-    max_blocks = block_table.shape[1]
-    bf16 = torch.bfloat16
-    dims = Dims(B, n_q, n_k, n_v, d_k, d_v, d_k ** -0.5 if scale is None else scale)
     if out is None:
-        out = torch.empty((B, n_q, d_v), dtype=bf16, device=q.device)
+        out = torch.empty((q.shape[0], q.shape[1], v_pages.shape[3]), dtype=torch.bfloat16, device=q.device)
     if workspace is None:
-        workspace = decode_workspace(dims, device=q.device)
-    st = lib().diffqkv_decode_paged_kv8(
-        dims, cache, _addr(q, "q", bf16, (B, n_q, d_k), dev),
-        _addr(block_table, "block_table", torch.int32, (B, max_blocks), dev), max_blocks,
-        _addr(seq_lens, "seq_lens", torch.int32, (B,), dev), 0 if max_seq_len is None else max_seq_len,
-        _addr(out, "out", bf16, (B, n_q, d_v), dev), _addr(workspace, "workspace", torch.uint8, workspace.shape, dev),
-        workspace.numel(), _stream_on(dev, stream))
+        workspace = decode_workspace(_kv8_dims(q, q.shape[0], k_pages, v_pages), device=q.device)
+    st = serving().decode_paged_kv8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, scale,
+                                    0 if max_seq_len is None else max_seq_len, out, workspace, stream)
     check(st, "diffqkv_decode_paged_kv8")
     return out
 
@@ -568,22 +493,12 @@ def prefill_paged_kv8(q: torch.Tensor, query_start: torch.Tensor, k_pages: torch
     owning rows query_start[b] .. query_start[b + 1] - 1 (int32 [B + 1], as :func:`page_map` writes it) at the last
     positions of its seq_lens[b] (int32 [B], the new rows included and stored).  Returns bf16 [tokens, n_q, d_v]; rows
     behind query_start[B] are not written."""
-    cache, dev, n_k, n_v, d_k, d_v = _kv8_cache(k_pages, v_pages, k_scales, v_scales)
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be [tokens, n_q, d_k] and block_table [B, max_blocks]")
-    T, n_q, _ = q.shape
-    B, max_blocks = block_table.shape
-    bf16, i32 = torch.bfloat16, torch.int32
-    dims = Dims(B, n_q, n_k, n_v, d_k, d_v, d_k ** -0.5 if scale is None else scale)
     if out is None:
-        out = torch.empty((T, n_q, d_v), dtype=bf16, device=q.device)
+        out = torch.empty((q.shape[0], q.shape[1], v_pages.shape[3]), dtype=torch.bfloat16, device=q.device)
     if workspace is None:
-        workspace = prefill_paged_kv8_workspace(dims, q.device)
-    st = lib().diffqkv_prefill_paged_kv8(
-        dims, cache, _addr(q, "q", bf16, (T, n_q, d_k), dev), _addr(query_start, "query_start", i32, (B + 1,), dev), T,
-        _addr(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks,
-        _addr(seq_lens, "seq_lens", i32, (B,), dev), _addr(out, "out", bf16, (T, n_q, d_v), dev),
-        _addr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(), _stream_on(dev, stream))
+        workspace = prefill_paged_kv8_workspace(_kv8_dims(q, block_table.shape[0], k_pages, v_pages), q.device)
+    st = serving().prefill_paged_kv8(q, query_start, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, scale, out,
+                                     workspace, stream)
     check(st, "diffqkv_prefill_paged_kv8")
     return out
 

@@ -148,6 +148,26 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_serving = None
+
+
+def serving():
+    """The extension that marshals the serving operators, bound to the loaded library's entry points."""
+    global _serving
+    if _serving is None:
+        h = lib()
+        try:
+            from . import _serving as ext
+        except ImportError as e:
+            raise RuntimeError("asymmetric_head_kv_b200/_serving.so is missing or does not load: build it with "
+                               "`python -m asymmetric_head_kv_b200.build`") from e
+        ext.bind(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value
+                   for n in ("diffqkv_page_map", "diffqkv_kv8_store", "diffqkv_decode_paged_kv8",
+                             "diffqkv_prefill_paged_kv8")))
+        _serving = ext
+    return _serving
+
+
 def check(status: int, what: str):
     if status != OK:
         raise DiffqkvError(status, what)

@@ -3,7 +3,8 @@
 Usage: ``python -m asymmetric_head_kv_b200.build`` (or ``build()`` from Python).
 Each .cu file under csrc/ compiles to an object in _build/ (in parallel) and
 they link into asymmetric_head_kv_b200/libdiffqkv.so.  Recompiles only what
-changed (source or any header newer than its object).
+changed (source or any header newer than its object).  The CPython extension that
+marshals the serving operators (binding/serving.cpp) is built with g++ next to it.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdiffqkv.so")
 LIB_CHECKED = os.path.join(PKG, "libdiffqkv_checked.so")
+BINDING_SRC = os.path.join(PKG, "binding", "serving.cpp")
+BINDING = os.path.join(PKG, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -74,10 +78,32 @@ def _build_one(lib: str, objdir: str, force: bool, verbose: bool, extra_flags) -
     return lib
 
 
+def _build_binding(force: bool) -> str:
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "diffqkv.h"), __file__]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
+           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
+           BINDING_SRC, "-o", tmp, "-L" + os.path.join(t, "lib"), "-Wl,-rpath," + os.path.join(t, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for serving.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: bool = True) -> str:
     """Builds libdiffqkv.so and, unless checked=False, libdiffqkv_checked.so: the same sources with
     -DDIFFQKV_BOUNDS_CHECK (device-side index checks; selected at run time by DIFFQKV_BOUNDS_CHECK=1)."""
     lib = _build_one(LIB, BUILD, force, verbose, extra_flags)
+    _build_binding(force)
     if checked:
         _build_one(LIB_CHECKED, BUILD + "_checked", force, verbose, tuple(extra_flags) + ("-DDIFFQKV_BOUNDS_CHECK",))
     return lib
