@@ -12,6 +12,9 @@
 // shared memory, and a token or page finds its request by a binary search over the runs and a walk
 // inside one.  No CTA reads what another writes: the slot of a token in a new page comes from the
 // free list, not from the table entry.
+// Up to kManyThreads requests a thread has one request, and what the tokens need of it (its length, its pages, the page that
+// it fills first, and the head of the free list) is fetched beside the sums and kept in shared memory: the map of a decode
+// step then has two dependent global loads in a row instead of five.
 #include "common.cuh"
 #include "internal.h"
 
@@ -19,13 +22,13 @@ namespace diffqkv {
 
 namespace {
 
-constexpr int kMapThreads = 512;
+constexpr int kFewThreads = 256, kManyThreads = 1024;
 constexpr int kMapTokens = 4;  // consecutive tokens a thread maps (one 16-byte store per output)
 
 struct PageMapArgs {
     const int32_t *seq_lens, *new_lens, *free_pages;
     int32_t *block_table, *query_start, *slot_map, *positions, *total_lens, *pages_used, *status;
-    int32_t batch, max_blocks, page_size, num_pages, num_free, capacity;
+    int32_t batch, max_blocks, page_size, page_shift, num_pages, num_free, capacity;
     int32_t per;  // requests of one thread's run
 };
 
@@ -33,6 +36,10 @@ struct Request {
     int s, n;      // cached positions and new tokens, after the checks
     int have, take;  // pages it holds and pages it takes
 };
+
+__device__ __forceinline__ int page_of(const PageMapArgs &a, int x) {
+    return a.page_shift >= 0 ? x >> a.page_shift : x / a.page_size;
+}
 
 // Request b after the checks: lengths outside [0, max_blocks * page_size] add nothing.
 __device__ __forceinline__ Request load_request(const PageMapArgs &a, int b, bool dropped, bool flag) {
@@ -43,14 +50,17 @@ __device__ __forceinline__ Request load_request(const PageMapArgs &a, int b, boo
     const bool bad = s < 0 || s > cap || n < 0 || n > cap - s;
     if (bad && flag) record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
     r.n = bad || dropped ? 0 : n;
-    r.have = r.s / a.page_size + (r.s % a.page_size != 0);
-    const int t = r.s + r.n;
-    r.take = t / a.page_size + (t % a.page_size != 0) - r.have;
+    auto pages = [&](int x) {
+        const int p = page_of(a, x);
+        return p + (x != p * a.page_size);
+    };
+    r.have = pages(r.s);
+    r.take = pages(r.s + r.n) - r.have;
     return r;
 }
 
 // Largest i in [0, n) with v[i] <= x (v ascending, v[0] <= x).
-__device__ __forceinline__ int last_not_above(const long long *v, int n, long long x) {
+__device__ __forceinline__ int last_not_above(const int *v, int n, int x) {
     int lo = 0;
     while (n > 1) {
         const int half = n >> 1;
@@ -60,20 +70,35 @@ __device__ __forceinline__ int last_not_above(const long long *v, int n, long lo
     return lo;
 }
 
-__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs a) {
-    __shared__ long long tok_s[kMapThreads + 1];  // tokens before each run
-    __shared__ long long pag_s[kMapThreads + 1];  // pages taken before each run
-    __shared__ long long warp_t[kMapThreads / 32], warp_p[kMapThreads / 32];
+// A pool page, or -1 (flagged) for an entry outside the pool.
+__device__ __forceinline__ int checked_page(const PageMapArgs &a, int page) {
+    if (page >= 0 && page < a.num_pages) return page;
+    record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+    return -1;
+}
+
+// ONE: at most THREADS requests, one a thread.
+template <int THREADS, bool ONE>
+__global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ int tok_s[THREADS], pag_s[THREADS];  // tokens and pages before each run
+    __shared__ long long warp_t[WARPS], warp_p[WARPS];
+    __shared__ int len_s[ONE ? THREADS : 1], page_s[ONE ? THREADS : 1], free_s[THREADS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b0 = min(a.batch, tid * a.per), b1 = min(a.batch, b0 + a.per);
     const bool first_cta = blockIdx.x == 0;
 
+    free_s[tid] = tid < a.num_free ? __ldg(a.free_pages + tid) : -1;
     long long t = 0, p = 0;
+    Request own{0, 0, 0, 0};
     for (int b = b0; b < b1; ++b) {
-        const Request r = load_request(a, b, false, first_cta);
-        t += r.n;
-        p += r.take;
+        own = load_request(a, b, false, first_cta);
+        t += own.n;
+        p += own.take;
     }
+    int own_page = -1;  // pool page of the position after the cached ones, where that page is held
+    if (ONE && b0 < b1 && own.n > 0 && page_of(a, own.s) < own.have)
+        own_page = a.block_table[(size_t)b0 * a.max_blocks + page_of(a, own.s)];
     long long it = t, ip = p;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -88,96 +113,126 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
         warp_p[warp] = ip;
     }
     __syncthreads();
-    long long bt = 0, bp = 0;
-    for (int w = 0; w < warp; ++w) {
-        bt += warp_t[w];
-        bp += warp_p[w];
+    // every warp scans the warps' sums
+    long long wt = lane < WARPS ? warp_t[lane] : 0, wp = lane < WARPS ? warp_p[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < WARPS; off <<= 1) {
+        const long long yt = __shfl_up_sync(0xffffffffu, wt, off), yp = __shfl_up_sync(0xffffffffu, wp, off);
+        if (lane >= off) {
+            wt += yt;
+            wp += yp;
+        }
     }
-    tok_s[tid] = bt + it - t;
-    pag_s[tid] = bp + ip - p;
-    if (tid == kMapThreads - 1) {
-        tok_s[kMapThreads] = bt + it;
-        pag_s[kMapThreads] = bp + ip;
-    }
-    __syncthreads();
+    const long long all_t = __shfl_sync(0xffffffffu, wt, WARPS - 1), all_p = __shfl_sync(0xffffffffu, wp, WARPS - 1);
+    const long long bt = __shfl_sync(0xffffffffu, wt, max(warp - 1, 0)), bp = __shfl_sync(0xffffffffu, wp, max(warp - 1, 0));
     // a step that does not fit the token buffer or the free list is dropped as a whole
-    const bool no_room = tok_s[kMapThreads] > a.capacity;
-    const bool dropped = no_room || pag_s[kMapThreads] > a.num_free;
+    const bool no_room = all_t > a.capacity;
+    const bool dropped = no_room || all_p > a.num_free;
     if (dropped && first_cta && tid == 0)
         record_error(a.status, no_room ? DIFFQKV_ERR_DEVICE_SEQLEN : DIFFQKV_ERR_DEVICE_PAGE);
-    const int tokens = dropped ? 0 : (int)tok_s[kMapThreads];
-    const int pages = dropped ? 0 : (int)pag_s[kMapThreads];
+    const int tokens = dropped ? 0 : (int)all_t, pages = dropped ? 0 : (int)all_p;
+    const int t_before = dropped ? 0 : (int)((warp ? bt : 0) + it - t), p_before = dropped ? 0 : (int)((warp ? bp : 0) + ip - p);
+    tok_s[tid] = t_before;
+    pag_s[tid] = p_before;
+    if (ONE) {
+        len_s[tid] = own.s;
+        page_s[tid] = own_page;
+    }
 
     // per-request outputs: run i belongs to CTA i mod grid
     if (tid % gridDim.x == blockIdx.x) {
-        int at = dropped ? 0 : (int)tok_s[tid];
+        int at = t_before;
         for (int b = b0; b < b1; ++b) {
-            const Request r = load_request(a, b, dropped, false);
+            if (!ONE) own = load_request(a, b, false, false);
+            if (dropped) own.n = 0;
             a.query_start[b] = at;
-            a.total_lens[b] = r.s + r.n;
-            at += r.n;
+            a.total_lens[b] = own.s + own.n;
+            at += own.n;
         }
     }
     if (first_cta && tid == 0) {
         a.query_start[a.batch] = tokens;
         a.pages_used[0] = pages;
     }
-    const int runs = (a.batch + a.per - 1) / a.per;
-    const int stride = gridDim.x * kMapThreads;
+    __syncthreads();
+    const int runs = ONE ? a.batch : (a.batch + a.per - 1) / a.per;
+    const int stride = gridDim.x * THREADS;
+    auto held_pages = [&](int s) {
+        const int q = page_of(a, s);
+        return q + (s != q * a.page_size);
+    };
+    auto free_page = [&](int k) { return k < THREADS ? free_s[k] : __ldg(a.free_pages + k); };
 
     // table entries of the pages taken
-    for (int k = blockIdx.x * kMapThreads + tid; k < pages; k += stride) {
+    for (int k = blockIdx.x * THREADS + tid; k < pages; k += stride) {
         const int run = last_not_above(pag_s, runs, k);
-        int b = run * a.per;
-        long long off = pag_s[run];
-        Request r = load_request(a, b, false, false);
-        while (k >= off + r.take) {
-            off += r.take;
-            r = load_request(a, ++b, false, false);
+        int b = run * a.per, off = pag_s[run], have;
+        if (ONE) {
+            have = held_pages(len_s[run]);
+        } else {
+            Request r = load_request(a, b, false, false);
+            while (k >= off + r.take) {
+                off += r.take;
+                r = load_request(a, ++b, false, false);
+            }
+            have = r.have;
         }
-        int page = __ldg(a.free_pages + k);
-        if (page < 0 || page >= a.num_pages) {
-            record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
-            page = -1;
-        }
-        a.block_table[(size_t)b * a.max_blocks + r.have + (int)(k - off)] = page;
+        a.block_table[(size_t)b * a.max_blocks + have + (k - off)] = checked_page(a, free_page(k));
     }
 
     // slots and positions, kMapTokens consecutive tokens a thread
-    for (long long i0 = (long long)(blockIdx.x * kMapThreads + tid) * kMapTokens; i0 < a.capacity;
+    for (long long i0 = (long long)(blockIdx.x * THREADS + tid) * kMapTokens; i0 < a.capacity;
          i0 += (long long)stride * kMapTokens) {
         int slot[kMapTokens], pos[kMapTokens];
 #pragma unroll
         for (int e = 0; e < kMapTokens; ++e) slot[e] = pos[e] = -1;
         if (i0 < tokens) {
-            const int run = last_not_above(tok_s, runs, i0);
-            int b = run * a.per;
-            long long at = tok_s[run];
-            long long off = pag_s[run];
-            Request r = load_request(a, b, false, false);
+            int run = last_not_above(tok_s, runs, (int)i0);
+            int b = run * a.per, at = tok_s[run], off = pag_s[run], s, have, end;
+            auto open = [&] {  // the request's length, pages and end (ONE)
+                s = len_s[run];
+                have = held_pages(s);
+                at = tok_s[run];
+                off = pag_s[run];
+                end = run + 1 < runs ? tok_s[run + 1] : tokens;
+            };
+            Request r{0, 0, 0, 0};
+            if (ONE)
+                open();
+            else {
+                r = load_request(a, b, false, false);
+                s = r.s;
+                have = r.have;
+                end = at + r.n;
+            }
             int seen = -1, page = -1;  // logical page last looked up, and its pool page
 #pragma unroll
             for (int e = 0; e < kMapTokens; ++e) {
-                const long long i = i0 + e;
+                const int i = (int)i0 + e;
                 if (i >= tokens) break;
-                while (i >= at + r.n) {
-                    at += r.n;
-                    off += r.take;
-                    r = load_request(a, ++b, false, false);
+                while (i >= end) {
                     seen = -1;
-                }
-                pos[e] = r.s + (int)(i - at);
-                const int lp = pos[e] / a.page_size;
-                if (lp != seen) {
-                    seen = lp;
-                    page = lp < r.have ? a.block_table[(size_t)b * a.max_blocks + lp]
-                                       : __ldg(a.free_pages + off + (lp - r.have));
-                    if (page < 0 || page >= a.num_pages) {
-                        record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
-                        page = -1;
+                    if (ONE) {
+                        b = ++run;
+                        open();
+                    } else {
+                        at = end;
+                        off += r.take;
+                        r = load_request(a, ++b, false, false);
+                        s = r.s;
+                        have = r.have;
+                        end = at + r.n;
                     }
                 }
-                if (page >= 0) slot[e] = page * a.page_size + pos[e] % a.page_size;
+                pos[e] = s + (i - at);
+                const int lp = page_of(a, pos[e]);
+                if (lp != seen) {
+                    seen = lp;
+                    page = checked_page(a, lp >= have                  ? free_page(off + (lp - have))
+                                           : ONE && lp == page_of(a, s) ? page_s[run]
+                                                                        : a.block_table[(size_t)b * a.max_blocks + lp]);
+                }
+                if (page >= 0) slot[e] = page * a.page_size + (pos[e] - lp * a.page_size);
             }
         }
         if (i0 + kMapTokens <= a.capacity) {
@@ -229,12 +284,21 @@ diffqkv_status_t page_map_launch(int32_t batch, const int32_t *seq_lens, const i
     a.num_pages = num_pages;
     a.num_free = num_free;
     a.capacity = capacity;
-    a.per = (batch + kMapThreads - 1) / kMapThreads;
-    // enough CTAs for one sweep over the tokens, at most two a SM
-    const long long want = ((long long)capacity + kMapThreads * kMapTokens - 1) / (kMapThreads * kMapTokens);
-    const long long most = 2LL * dev.num_sms;
+    a.page_shift = -1;
+    if ((page_size & (page_size - 1)) == 0)
+        for (a.page_shift = 0; (1 << a.page_shift) < page_size;) ++a.page_shift;
+    const int threads = batch <= kFewThreads ? kFewThreads : kManyThreads;
+    a.per = (batch + threads - 1) / threads;
+    // enough CTAs for one sweep over the tokens, at most as many as the SMs hold
+    const long long want = ((long long)capacity + threads * kMapTokens - 1) / (threads * kMapTokens);
+    const long long most = (long long)dev.num_sms * (threads == kFewThreads ? 4 : 1);
     const int grid = (int)(want < 1 ? 1 : want > most ? most : want);
-    page_map_kernel<<<grid, kMapThreads, 0, stream>>>(a);
+    if (batch <= kFewThreads)
+        page_map_kernel<kFewThreads, true><<<grid, kFewThreads, 0, stream>>>(a);
+    else if (batch <= kManyThreads)
+        page_map_kernel<kManyThreads, true><<<grid, kManyThreads, 0, stream>>>(a);
+    else
+        page_map_kernel<kManyThreads, false><<<grid, kManyThreads, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? DIFFQKV_OK : DIFFQKV_ERR_CUDA;
 }
 

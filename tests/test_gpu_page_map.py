@@ -44,6 +44,7 @@ def _step(batch, hi, new_hi, page, seed, spare=3):
 @pytest.mark.parametrize("batch,hi,new_hi,page", [
     (1, 0, 1, 16), (1, 100, 1, 16), (1, 0, 5000, 8), (3, 33, 7, 1), (17, 500, 40, 24), (511, 60, 9, 16), (512, 60, 9, 16),
     (513, 60, 9, 16), (1500, 300, 30, 32), (2, 7, 0, 16),
+    (256, 90, 300, 16), (257, 90, 300, 16), (1023, 40, 90, 8), (1024, 40, 90, 24), (1025, 40, 90, 8),
 ])
 def test_against_the_definition(cuda_device, batch, hi, new_hi, page):
     s, n, table, free, num_pages = _step(batch, hi, new_hi, page, batch * 7 + page)
