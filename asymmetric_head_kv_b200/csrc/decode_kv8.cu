@@ -145,9 +145,9 @@ struct Misc {
     uint64_t k_full[3], k_empty[3], v_full[kMaxVSlots], v_empty[kMaxVSlots];
     uint64_t s_full[2], p_full[2], pv_done[2], q_ready[2], sc_full[kScaleWarps], sc_empty[kScaleWarps], mma_done;
     long long scan[4];
-    float red[2][4][16];     // [tile parity][warp][head]: maxima
+    alignas(16) float red[2][4][16];  // [tile parity][warp][head]: maxima
     float l_red[4][16];
-    float q_scale[2][16];    // [unit parity][head]: scale * log2(e) * 2^(the query's exponent)
+    alignas(16) float q_scale[2][16];  // [unit parity][head]: scale * log2(e) * 2^(the query's exponent)
     uint32_t tmem_slot;
     int abort_flag, last_flag;
 };
@@ -468,20 +468,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         float l[QPK];                    // this position's share of the row sums
         float m_ref = 0.f, R = 0.f;      // lane h: head h's references (the same in the four warps)
-        int vl[QPK];                     // V head of each query head inside the group
-        int unit = -1;
+        uint32_t vls[(QPK + 7) / 8] = {};  // V head of each query head inside the group, four bits each
+        auto vl = [&](int h) { return (int)(vls[h >> 3] >> (4 * (h & 7)) & 15u); };
+        int unit = -1, my_vl = 0;        // (lane h's own)
         for (int k = 0; k < n_tiles; ++k) {
             const bool start = k == 0 || w.i == 0;
             const int slot = k % kScaleWarps;
             if (start) {
                 ++unit;
                 mbar_wait_bounded(&ms.q_ready[unit & 1], (uint32_t)(unit >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
-                const int v0 = w.g * QPK / a.q_per_v;
+                // (a division a lane instead of one a head)
+                const int mine = lane < QPK ? (w.g * QPK + lane) / a.q_per_v - w.g * QPK / a.q_per_v : 0;
+                my_vl = mine;
 #pragma unroll
-                for (int h = 0; h < QPK; ++h) {
-                    vl[h] = (w.g * QPK + h) / a.q_per_v - v0;
-                    l[h] = 0.f;
+                for (int i = 0; i < (QPK + 7) / 8; ++i) {
+                    vls[i] = 0;
+#pragma unroll
+                    for (int h = 8 * i; h < QPK && h < 8 * i + 8; ++h)
+                        vls[i] |= (uint32_t)__shfl_sync(0xffffffffu, mine, h) << (4 * (h & 7));
                 }
+#pragma unroll
+                for (int h = 0; h < QPK; ++h) l[h] = 0.f;
             }
             const int valid = min(kTT, w.T - w.i * kTT);
             mbar_wait_bounded(&ms.sc_full[slot], (uint32_t)(k / kScaleWarps & 1), a.wait_limit_ns, abort_flag, a.status);
@@ -490,8 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float kf = exp2_int(ke[tid]);
             float vx[QPK];
 #pragma unroll
-            for (int h = 0; h < QPK; ++h) vx[h] = (float)ve[vl[h] * kTT + tid] + kTop;
-            const int my_vl = lane < QPK ? (w.g * QPK + lane) / a.q_per_v - w.g * QPK / a.q_per_v : 0;
+            for (int h = 0; h < QPK; ++h) vx[h] = (float)ve[vl(h) * kTT + tid] + kTop;
             const float vm = (float)reinterpret_cast<const int *>(sc_s + slot * a.sc_bytes + kTT * (1 + a.vpg))[my_vl];
             mbar_wait_bounded(&ms.s_full[k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
@@ -513,9 +519,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float m[QPK];
 #pragma unroll
                 for (int h = 0; h < QPK; ++h) m[h] = warp_max(s[h]);
-                if (lane == 0)
+                if (lane == 0) {
 #pragma unroll
-                    for (int h = 0; h < QPK; ++h) ms.red[k & 1][warp][h] = m[h];
+                    for (int h = 0; h < QPK; h += 4) {
+                        if constexpr (QPK >= 4)
+                            *reinterpret_cast<float4 *>(&ms.red[k & 1][warp][h]) =
+                                make_float4(m[h], m[h + 1], m[h + 2], m[h + 3]);
+                        else
+#pragma unroll
+                            for (int e = 0; e < QPK; ++e) ms.red[k & 1][warp][e] = m[e];
+                    }
+                }
             }
             named_barrier(1, kSoftmaxThreads);
             // lane h moves head h's references where the tile exceeds them
@@ -542,11 +556,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                                   a.status);
                 tc_fence_after();
 #pragma unroll
+                for (int h = 0; h < QPK; ++h) l[h] *= __shfl_sync(0xffffffffu, l_scale, h);
+#pragma unroll 1
                 for (int h = 0; h < QPK; ++h) {
-                    l[h] *= __shfl_sync(0xffffffffu, l_scale, h);
                     const float f = __shfl_sync(0xffffffffu, alpha, h);
+                    const int v = __shfl_sync(0xffffffffu, my_vl, h);
                     if (f == 1.f) continue;
-                    const uint32_t at = t_o + (uint32_t)o_column(h, vl[h], w.g);
+                    const uint32_t at = t_o + (uint32_t)o_column(h, v, w.g);
                     uint32_t r[2], r2[1];
                     tmem_ld_cols<2>(at, r);
                     tmem_ld_cols<1>(at + 2, r2);
@@ -606,23 +622,36 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tc_fence_after();
                 const long long u = (long long)w.b * a.n_k + w.g;
                 const long long first = cta_of_tile(w.P, N, Ge), last = cta_of_tile(w.P + w.nt - 1, N, Ge);
+                const bool whole = first == last;  // no other CTA has a piece: straight to the output
                 const bool slot_ok = in_bounds(u + c, a.partial_slots, a.status);
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < QPK; ++h) {
                     uint32_t r[4];
-                    tmem_ld_cols<4>(t_o + (uint32_t)o_column(h, vl[h], w.g), r);
+                    tmem_ld_cols<4>(t_o + (uint32_t)o_column(h, __shfl_sync(0xffffffffu, my_vl, h), w.g), r);
                     tmem_wait_ld();
                     const float o = fmaf(fmaf(__uint_as_float(r[2]), 0.03125f, __uint_as_float(r[1])), 0.03125f,
                                          __uint_as_float(r[0]));
-                    float *dst = a.partials + ((size_t)(u + c) * QPK + h) * (DV + kPad);
                     const float m_h = __shfl_sync(0xffffffffu, m_ref, h), r_h = __shfl_sync(0xffffffffu, R, h);
-                    if (slot_ok) {
-                        if (tid < DV) __stcg(dst + tid, o * exp2f(r_h - kTop - m_h));
+                    const float l_h = ms.l_red[0][h] + ms.l_red[1][h] + ms.l_red[2][h] + ms.l_red[3][h];
+                    const float o_rel = o * exp2f(r_h - kTop - m_h);  // relative to 2^m
+                    if (whole) {
+                        const long long row = (long long)w.b * a.n_q + w.g * QPK + h;
+                        if (tid < DV && in_bounds(row, (long long)a.batch * a.n_q, a.status))
+                            a.out[row * DV + tid] = __float2bfloat16_rn(o_rel / l_h);
+                    } else if (slot_ok) {
+                        float *dst = a.partials + ((size_t)(u + c) * QPK + h) * (DV + kPad);
+                        if (tid < DV) __stcg(dst + tid, o_rel);
                         if (tid == 0) {
                             __stcg(dst + DV, m_h);
-                            __stcg(dst + DV + 1, ms.l_red[0][h] + ms.l_red[1][h] + ms.l_red[2][h] + ms.l_red[3][h]);
+                            __stcg(dst + DV + 1, l_h);
                         }
                     }
+                }
+                if (whole) {
+                    tc_fence_before();
+                    named_barrier(1, kSoftmaxThreads);  // l_red is written again by the next unit
+                    walker_advance<kTT>(w, a);
+                    continue;
                 }
                 tc_fence_before();
                 __threadfence();
@@ -641,31 +670,34 @@ __global__ void __launch_bounds__(kThreads, 2)
                         auto rec = [&](long long cc) {
                             return a.partials + ((size_t)(u + cc) * QPK + h2) * (DV + kPad);
                         };
-                        float M = -INFINITY;
-                        for (long long c0 = first; c0 <= last; c0 += 8) {
-                            float mv[8];
+                        // records four at a time; the maximum first, unless four are all
+                        float M = -INFINITY, L = 0.f;
+                        if (last - first >= 4)
+                            for (long long c0 = first; c0 <= last; c0 += 8) {
+                                float mv[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) mv[e] = c0 + e <= last ? __ldcg(rec(c0 + e) + DV) : -INFINITY;
+                                for (int e = 0; e < 8; ++e) mv[e] = c0 + e <= last ? __ldcg(rec(c0 + e) + DV) : -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) M = fmaxf(M, mv[e]);
-                        }
-                        float L = 0.f;
+                                for (int e = 0; e < 8; ++e) M = fmaxf(M, mv[e]);
+                            }
                         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (long long c0 = first; c0 <= last; c0 += 4) {
-                            float mv[4], lv[4];
+                            float2 ml[4];
                             float4 xv[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
+                            for (int e = 0; e < 4; ++e) {
+                                ml[e] = make_float2(-INFINITY, 0.f);
                                 if (c0 + e <= last) {
-                                    mv[e] = __ldcg(rec(c0 + e) + DV);
-                                    lv[e] = __ldcg(rec(c0 + e) + DV + 1);
+                                    ml[e] = __ldcg(reinterpret_cast<const float2 *>(rec(c0 + e) + DV));
                                     xv[e] = __ldcg(reinterpret_cast<const float4 *>(rec(c0 + e)) + d4);
                                 }
+                            }
+                            if (last - first < 4) M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 if (c0 + e > last) break;
-                                const float f = fast_exp2(mv[e] - M);
-                                L = fmaf(f, lv[e], L);
+                                const float f = fast_exp2(ml[e].x - M);
+                                L = fmaf(f, ml[e].y, L);
                                 O.x = fmaf(f, xv[e].x, O.x);
                                 O.y = fmaf(f, xv[e].y, O.y);
                                 O.z = fmaf(f, xv[e].z, O.z);
