@@ -84,7 +84,7 @@ struct Cfg {
 
 struct Misc {
     uint64_t raw_full[kRaw], raw_empty[kRaw], cv_full[3], cv_empty[3], sc_full[kScaleSlots], sc_empty[kScaleSlots];
-    uint64_t q_full, s_full[QT][2], p_full[QT], pv_done[QT], mma_done;
+    uint64_t q_full, s_full[QT][2], p_full[QT][2], pv_done[QT][2], mma_done;
     uint32_t k_mul[kScaleSlots][BN], v_mul[kScaleSlots][BN];  // 2^(e - e_ref) as f16 pairs, 0 behind the sequence
     int k_ref[kScaleSlots], v_ref[kScaleSlots];               // e_ref
     int ref[3][2];                                            // the same by converted stage: K, V
@@ -190,45 +190,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int h = blockIdx.x % a.n_q;
 
-    // ---- the unit: 256-row blocks of all requests, the last (longest context) first
+    // ---- the unit: 256-row blocks of all requests, the heaviest first: up to 32 requests by their length, more in the
+    // reverse of their order; a request's last block (the longest context) first
     if (warp == 0) {
-        int total = 0;
-        for (int pass = 0; pass < 2; ++pass) {
-            const int want = total - 1 - (int)(blockIdx.x / a.n_q);  // (second pass)
-            int acc = 0;
-            if (pass == 1 && lane == 0) ms.found[0] = -1;
-            __syncwarp();
-            for (int base = 0; base < a.batch; base += 32) {
-                const int b = base + lane;
-                int2 r = make_int2(0, 0);
-                if (b < a.batch) {
-                    r = request_rows(a, b);
-                    if (pass == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
-                        const int raw_s = __ldg(a.query_start + b), raw_e = __ldg(a.query_start + b + 1);
-                        const int T = __ldg(a.seq_lens + b);
-                        if (raw_s < 0 || raw_e < raw_s || raw_e > a.tokens || T < 0 || T > a.t_max || r.y > T)
-                            record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
-                    }
-                }
-                const int n = (r.y + kRows - 1) / kRows;
+        const bool flags = blockIdx.x == 0 && blockIdx.y == 0;
+        auto look = [&](int b, int2 &r, int &T) {  // blocks of request b
+            r = make_int2(0, 0);
+            T = 0;
+            if (b >= a.batch) return 0;
+            r = request_rows(a, b);
+            const int raw_T = __ldg(a.seq_lens + b);
+            T = clamp_to(raw_T, a.t_max);
+            if (flags) {
+                const int raw_s = __ldg(a.query_start + b), raw_e = __ldg(a.query_start + b + 1);
+                if (raw_s < 0 || raw_e < raw_s || raw_e > a.tokens || raw_T != T || r.y > raw_T)
+                    record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
+            }
+            return (r.y + kRows - 1) / kRows;
+        };
+        auto found = [&](int b, int block, const int2 &r, int T) {
+            ms.found[0] = b;
+            ms.found[1] = block;
+            ms.found[2] = r.x;
+            ms.found[3] = r.y;
+            ms.found[4] = T;
+        };
+        const int want = (int)(blockIdx.x / a.n_q);
+        if (lane == 0) ms.found[0] = -1;
+        __syncwarp();
+        int2 r;
+        int T;
+        if (a.batch <= 32) {
+            const int n = look(lane, r, T);
+            int before = 0;
+            for (int j = 0; j < a.batch; ++j) {
+                const int Tj = __shfl_sync(0xffffffffu, T, j), nj = __shfl_sync(0xffffffffu, n, j);
+                if (Tj > T || (Tj == T && j > lane)) before += nj;
+            }
+            if (want >= before && want < before + n) found(lane, n - 1 - (want - before), r, T);
+        } else {
+            int after = 0;  // blocks of the requests behind this group of 32
+            for (int base = (a.batch - 1) / 32 * 32; base >= 0; base -= 32) {
+                const int n = look(base + lane, r, T);
                 int incl = n;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += y;
+                    const int y = __shfl_down_sync(0xffffffffu, incl, off);
+                    if (lane + off < 32) incl += y;
                 }
-                const int before = acc + incl - n;
-                if (pass == 1 && n > 0 && want >= before && want < before + n) {
-                    ms.found[0] = b;
-                    ms.found[1] = want - before;
-                    ms.found[2] = r.x;
-                    ms.found[3] = r.y;
-                    ms.found[4] = clamp_to(__ldg(a.seq_lens + b), a.t_max);
-                }
-                acc += __shfl_sync(0xffffffffu, incl, 31);
+                const int before = after + incl - n;
+                if (want >= before && want < before + n) found(base + lane, n - 1 - (want - before), r, T);
+                after += __shfl_sync(0xffffffffu, incl, 0);
             }
-            if (pass == 0) total = acc;
-            __syncwarp();
         }
     }
     __syncthreads();
@@ -275,8 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < QT; ++t) {
             mbar_init(&ms.s_full[t][0], 1);
             mbar_init(&ms.s_full[t][1], 1);
-            mbar_init(&ms.p_full[t], 8);
-            mbar_init(&ms.pv_done[t], 1);
+            mbar_init(&ms.p_full[t][0], 8);
+            mbar_init(&ms.p_full[t][1], 8);
+            mbar_init(&ms.pv_done[t][0], 1);
+            mbar_init(&ms.pv_done[t][1], 1);
         }
         mbar_init(&ms.mma_done, 1);
         ms.abort_flag = 0;
@@ -466,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
                     if (n - 1 >= end[t]) continue;
-                    mbar_wait_bounded(&ms.p_full[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+                    mbar_wait_bounded(&ms.p_full[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
                     tc_fence_after();
                     const uint32_t t_p = tmem + (uint32_t)(t * 2 * BN + ((k - 1) & 1) * BN);
                     if (elect_one()) {
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int ks = 0; ks < BN / 16; ++ks)
                             umma_bf16_tmem_a(tmem + T_O + (uint32_t)(t * DV), t_p + ks * 8, vd + ks * (16 * 128 >> 4),
                                              idesc_pv, ks > 0 ? 1u : onto);
-                        umma_commit(&ms.pv_done[t]);
+                        umma_commit(&ms.pv_done[t][(k - 1) & 1]);
                     }
                     __syncwarp();
                 }
@@ -583,7 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_used = m_new == -INFINITY ? 0.f : m_new;
                     v_run = v_ref;
                 } else {
-                    mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+                    // (S of tile k has been waited for, so P.V of tiles up to k - 2 is done: k - 1 is this barrier's next phase)
+                    mbar_wait_bounded(&ms.pv_done[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
+                                      a.status);
                     tc_fence_after();
                     const bool grow = m_new > m_used + kRescale;
                     const float lf = grow ? fast_exp2(m_used - m_new) : 1.f;
@@ -622,15 +639,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2_unpack(f2_add(l2[0], l2[1]), la, lb);
             l += la + lb;
             tmem_wait_st();
-            // at most one P.V behind, so that every phase of pv_done is waited for in turn
-            if (k >= 1) mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((k - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.p_full[t]);
+            if (lane == 0) mbar_arrive(&ms.p_full[t][k & 1]);
         }
         const int done = end[t] - n0;
         if (done > 0) {
-            mbar_wait_bounded(&ms.pv_done[t], (uint32_t)((done - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
+            mbar_wait_bounded(&ms.pv_done[t][(done - 1) & 1], (uint32_t)((done - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
+                              a.status);
             tc_fence_after();
         }
         ms.row_s[t][half][r] = l;
