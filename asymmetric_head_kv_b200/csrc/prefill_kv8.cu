@@ -5,20 +5,29 @@
 // with p_r the row's position, kc, vc the e4m3 codes and ke, ve the exponents of their blocks.  A dense contraction,
 // 2 (d_k + d_v) operations for every row, head and position, on tcgen05 kind::f16:
 //
-//  * One CTA takes 256 query rows of one request and head as two 128-row tiles that share every 64-position K/V
-//    tile.  Four warps turn a tile's codes into f16 once for both: code * 2^(e - e_ref), with e_ref the tile's largest
-//    exponent for K and the largest so far for V, which is exact unless a block's scale is 2^15 below it.  (Feeding codes to fp8 MMAs instead
+//  * One CTA takes 256 query rows of one request and head as two 128-row tiles that share every 64-position K/V tile
+//    (128-position tiles, whose S cannot be double-buffered in TMEM: 766 us where these take 500).  Four warps turn a
+//    tile's codes into f16 once for both: code * 2^(e - e_ref), with e_ref the tile's largest exponent for K and the
+//    largest so far for V, which is exact unless a block's scale is 2^15 below it.  (Feeding codes to fp8 MMAs instead
 //    would split every softmax weight into e4m3 terms, five more instructions for each pair of scores in the warps that
-//    bound this kernel; conversion costs the tile 12 instructions for 16 codes in warps that have nothing else
-//    to do.)  K's e_ref goes into the scores' multiplier; when V's grows, O is rescaled.
+//    bound this kernel; conversion costs the tile 12 instructions for 16 codes in warps that have nothing else to do.)
+//    K's e_ref goes into the scores' multiplier; when V's grows, O is rescaled.
 //  * Queries are scaled by a power of two per row into f16's range (8 significant bits fit its 11).
-//  * Softmax warps own a row per thread; S is double-buffered in TMEM, P (f16) goes back over S and is the A
-//    operand of P.V; O is rescaled in TMEM only when a row's maximum grows by 2^8 or V's exponent grows.
-//    Weights are held at 2^7 of the reference, so that f16 resolves 2^-31 of the largest.
+//  * Softmax: two threads a row, 32 columns each, so that four warps a scheduler hide one another's latencies; S is
+//    double-buffered in TMEM, P (f16) goes back over S and is the A operand of P.V; O is rescaled in TMEM only when a
+//    row's maximum grows by 2^8 or V's exponent grows.  Weights are held at 2^7 of the reference, so that f16 resolves
+//    2^-31 of the largest; their sum is fp32, of the unrounded weights.
 //  * MMA, commit and TMA are issued by an elected lane (kv8.cuh).
-//  * Few rows over a long context: the K/V tiles of a unit are cut into equal splits over the SMs that have no unit of
-//    their own; partials in the workspace, merged by the last CTA of the unit.
-// What bounds it: the 64 exponentials a row and tile (16 a clock and SM) and the softmax warps' latencies.
+//  * Rows of Q come in, and rows of the output go out, with a row's 16-byte pieces in neighbouring lanes.
+//  * Units are taken longest first.  Where they are fewer than half of the SMs, each is cut into pieces of equal length, one
+//    CTA each; records in the workspace, merged by the last CTA of the unit: 256 rows over 131072 positions, 16 heads, in
+//    270 us with 9 pieces a unit, 527 with 4.
+//    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
+//    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
+// What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 495 us, 832 TFLOP/s, 0.49 of the measured GEMM peak (tensor
+// pipe 35% busy, XU 47%, 53% of issue slots); 4 rows-of-17 requests of 1003 positions: 20.7 us, of which about 14 are one
+// CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -39,7 +48,8 @@ constexpr int kLoadWarp = 16, kMmaWarp = 17, kScaleWarp = 18, kConvWarp0 = 19, k
 constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kRaw = 4;         // stages of codes
 constexpr int kScaleSlots = 8;  // tiles of scales, fetched four at a time
-constexpr int kSlots = 160;     // partial records of the workspace (a CTA of a split unit each)
+constexpr int kSlots = 160;     // partial records of the workspace: one for each piece of a call whose units are cut
+constexpr int kCutBatch = 32;   // requests, at most, of a call whose units are cut
 constexpr int kHeader = 256;
 constexpr float kRescale = 8.f;  // growth (log2) of a row's maximum before O is rescaled
 constexpr float kShift = 7.f;    // weights are held at 2^kShift of the reference
@@ -54,7 +64,7 @@ struct PreArgs {
     int32_t *status;
     int32_t batch, n_q, n_k, n_v, tokens, t_max, max_blocks;
     int32_t page_size, page_shift, num_pages, sb, sub_rows, sub_shift;
-    int32_t splits;
+    int32_t max_pieces;  // of a call whose units are cut, 0: they are not
     long long scale_blocks;
     float scale_log2;
     uint64_t wait_limit_ns;
@@ -77,6 +87,7 @@ struct Cfg {
     static constexpr int RAW_K = BN * DK, RAW_V = BN * DV, RAW = RAW_K + RAW_V;
     static constexpr int K_BYTES = 2 * RAW_K, V_BYTES = 2 * RAW_V, CONV = K_BYTES + V_BYTES;
     static constexpr int STAGES = DK == 64 ? 3 : 2;   // converted tiles
+    static constexpr int REC = kRows * (DV + 2);      // floats of a partial record
     static constexpr int OFF_CONV = QT * Q_BYTES;
     static constexpr int OFF_RAW = OFF_CONV + STAGES * CONV;
     static constexpr int OFF_MISC = OFF_RAW + kRaw * RAW;
@@ -89,7 +100,7 @@ struct Misc {
     int k_ref[kScaleSlots], v_ref[kScaleSlots];               // e_ref
     int ref[3][2];                                            // the same by converted stage: K, V
     float row_s[QT][2][BM];                                   // exchange between the two halves of a row
-    int found[8];                                             // unit: b, block, q row, rows, length; total blocks
+    int found[8];  // unit: request, block, q row, rows, length; its pieces, which of them, its first record
     uint32_t tmem_slot;
     int abort_flag, last_flag;
 };
@@ -178,6 +189,86 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
     return r != 0;
 }
 
+// The rows of a unit from the records of its pieces, in the order of its tiles.  A thread takes kItems (row, four columns)
+// at once and the records kAhead at a time: one after the other, the loads' latency made it 40 us for 256 rows.
+template <int DV, int kItems, int kAhead>
+__device__ __forceinline__ void merge_pieces(const PreArgs &a, int record, int n, int q0, int rows, int h, int tid) {
+    constexpr size_t kRec = (size_t)kRows * (DV + 2);
+    // a warp: 8 rows by 4 fours of columns, whole sectors in the records (columns by fours ahead of rows) and in the output
+    const int r8 = (rows + 7) >> 3, items = r8 * DV * 2;
+    auto row_of = [&](int e) { return (e >> 5) % r8 * 8 + (e & 7); };
+    auto col_of = [&](int e) { return (e >> 5) / r8 * 4 + (e >> 3 & 3); };
+    for (int e0 = tid; e0 < items; e0 += kItems * kThreads) {
+        float M[kItems], L[kItems];
+        float4 x[kItems];
+        int at_o[kItems], at_ml[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int e = min(e0 + k * kThreads, items - 1), col = col_of(e), r = min(row_of(e), rows - 1);
+            M[k] = -INFINITY;
+            L[k] = 0.f;
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            at_o[k] = (col * kRows + r) * 4;
+            at_ml[k] = DV * kRows + 2 * r;
+        }
+#pragma unroll kAhead
+        for (int s = 0; s < n; ++s) {
+            const float *rec = a.partials + (size_t)(record + s) * kRec;
+            float2 ml[kItems];
+            float4 o[kItems];
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(rec + at_ml[k]));
+                o[k] = __ldcg(reinterpret_cast<const float4 *>(rec + at_o[k]));
+            }
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                if (ml[k].x == -INFINITY) continue;  // nothing of this piece is seen by the row
+                const float m = fmaxf(M[k], ml[k].x), f = fast_exp2(M[k] - m), g = fast_exp2(ml[k].x - m);
+                M[k] = m;
+                L[k] = fmaf(f, L[k], g * ml[k].y);
+                x[k].x = fmaf(f, x[k].x, g * o[k].x);
+                x[k].y = fmaf(f, x[k].y, g * o[k].y);
+                x[k].z = fmaf(f, x[k].z, g * o[k].z);
+                x[k].w = fmaf(f, x[k].w, g * o[k].w);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int e = e0 + k * kThreads, col = col_of(e), r = row_of(e);
+            if (e >= items || r >= rows) continue;
+            const float inv = M[k] == -INFINITY ? 0.f : 1.f / L[k];
+            *reinterpret_cast<uint2 *>(a.out + ((size_t)(q0 + r) * a.n_q + h) * DV + col * 4) =
+                make_uint2(pack_bf16x2(x[k].x * inv, x[k].y * inv), pack_bf16x2(x[k].z * inv, x[k].w * inv));
+        }
+    }
+}
+
+// Number of pieces that the blocks of this lane's request (n blocks of 256 of its last `rows` positions of T) are cut into.
+// All lanes hold a request each; lane l looks at pieces of at most 1 / (l + 1) of the longest unit, and the lane whose
+// longest piece is shortest wins, if every piece has an SM.  A piece takes kPieceCost tiles besides its own, more where its
+// rows are merged.
+__device__ __forceinline__ int cut_units(const PreArgs &a, int n, int rows, int T, int lane) {
+    constexpr int kPieceCost = 6, kCutCost = 2, kRowCost = 32;  // (rows of a merge that cost a tile)
+    const int tiles = n > 0 ? (T - 1) / BN + 1 : 0;  // of its last block
+    const int longest = max(1, __reduce_max_sync(0xffffffffu, tiles));
+    // (s = ceil(tiles / most) in floats: any s would be right, and all CTAs work out the same)
+    auto cut = [&](int t, float per) { return max(1, (int)ceilf((float)t * per - 1e-3f)); };
+    const float per = (float)(lane + 1) / (float)longest;
+    int count = 0, time = 0;
+    for (int j = 0; j < a.batch; ++j) {
+        const int nj = __shfl_sync(0xffffffffu, n, j), tj = __shfl_sync(0xffffffffu, tiles, j);
+        const int rj = __shfl_sync(0xffffffffu, rows, j);
+        if (nj == 0) continue;
+        const int s = cut(tj, per);
+        count += nj * s;
+        time = max(time, (int)__fdividef((float)tj, (float)s) + kPieceCost + (s > 1 ? kCutCost + min(rj, kRows) / kRowCost : 0));
+    }
+    if ((long long)count * a.n_q > a.max_pieces) time = lane == 0 ? 0x3ffffff : 0x7ffffff;  // lane 0 cuts nothing
+    const int best = (int)__reduce_min_sync(0xffffffffu, (uint32_t)min(time, 0x7ffffff) * 32u + (uint32_t)lane) & 31;
+    return cut(tiles, (float)(best + 1) / (float)longest);
+}
+
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kv8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -188,90 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc &ms = *reinterpret_cast<Misc *>(smem + C::OFF_MISC);
     volatile int *abort_flag = &ms.abort_flag;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    const int h = blockIdx.x % a.n_q;
-
-    // ---- the unit: 256-row blocks of all requests, the heaviest first: up to 32 requests by their length, more in the
-    // reverse of their order; a request's last block (the longest context) first
-    if (warp == 0) {
-        const bool flags = blockIdx.x == 0 && blockIdx.y == 0;
-        auto look = [&](int b, int2 &r, int &T) {  // blocks of request b
-            r = make_int2(0, 0);
-            T = 0;
-            if (b >= a.batch) return 0;
-            r = request_rows(a, b);
-            const int raw_T = __ldg(a.seq_lens + b);
-            T = clamp_to(raw_T, a.t_max);
-            if (flags) {
-                const int raw_s = __ldg(a.query_start + b), raw_e = __ldg(a.query_start + b + 1);
-                if (raw_s < 0 || raw_e < raw_s || raw_e > a.tokens || raw_T != T || r.y > raw_T)
-                    record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
-            }
-            return (r.y + kRows - 1) / kRows;
-        };
-        auto found = [&](int b, int block, const int2 &r, int T) {
-            ms.found[0] = b;
-            ms.found[1] = block;
-            ms.found[2] = r.x;
-            ms.found[3] = r.y;
-            ms.found[4] = T;
-        };
-        const int want = (int)(blockIdx.x / a.n_q);
-        if (lane == 0) ms.found[0] = -1;
-        __syncwarp();
-        int2 r;
-        int T;
-        if (a.batch <= 32) {
-            const int n = look(lane, r, T);
-            int before = 0;
-            for (int j = 0; j < a.batch; ++j) {
-                const int Tj = __shfl_sync(0xffffffffu, T, j), nj = __shfl_sync(0xffffffffu, n, j);
-                if (Tj > T || (Tj == T && j > lane)) before += nj;
-            }
-            if (want >= before && want < before + n) found(lane, n - 1 - (want - before), r, T);
-        } else {
-            int after = 0;  // blocks of the requests behind this group of 32
-            for (int base = (a.batch - 1) / 32 * 32; base >= 0; base -= 32) {
-                const int n = look(base + lane, r, T);
-                int incl = n;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int y = __shfl_down_sync(0xffffffffu, incl, off);
-                    if (lane + off < 32) incl += y;
-                }
-                const int before = after + incl - n;
-                if (want >= before && want < before + n) found(base + lane, n - 1 - (want - before), r, T);
-                after += __shfl_sync(0xffffffffu, incl, 0);
-            }
-        }
-    }
-    __syncthreads();
-    const int b = ms.found[0];
-    if (b < 0) return;
-    const int row0 = ms.found[1] * kRows, n_rows = ms.found[3], T = ms.found[4];
-    const int first = T - n_rows;  // position of the request's first row
-    const int q0 = ms.found[2] + row0;
-    const int kh = h / (a.n_q / a.n_k), vh = h / (a.n_q / a.n_v);
-
-    int n_kv[QT];  // K/V tiles that a query tile's rows see
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const int rows = min(n_rows - row0 - t * BM, BM);
-        const int last = first + row0 + t * BM + rows - 1;
-        n_kv[t] = uniform(rows > 0 && last >= 0 ? last / BN + 1 : 0);
-    }
-    const int n_all = max(n_kv[0], n_kv[1]);
-    const int chunk = (n_all + a.splits - 1) / a.splits;
-    const int n0 = blockIdx.y * chunk, n1 = min(n_all, n0 + chunk);
-    if (n_all == 0 || n0 >= n1) {
-        if (n_all == 0 && blockIdx.y == 0)  // rows without a position
-            for (int e = tid; e < min(n_rows - row0, kRows) * (DV / 8); e += kThreads)
-                *reinterpret_cast<uint4 *>(a.out + ((size_t)(q0 + e / (DV / 8)) * a.n_q + h) * DV + e % (DV / 8) * 8) =
-                    make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const int end[QT] = {min(n_kv[0], n1), min(n_kv[1], n1)};
-
-    if (tid == 0) {
+    if (tid == 32) {
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(&ms.raw_full[s], 1);
             mbar_init(&ms.raw_empty[s], kConvWarps);
@@ -298,6 +306,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         ms.last_flag = 0;
         fence_barrier_init();
     }
+    // ---- the piece: of a unit (256-row block, head), heaviest first: up to 32 requests by their length, more in the reverse
+    // of their order; a request's last block (the longest context) first, the pieces of a block side by side
+    if (warp == 0) {
+        const bool flags = blockIdx.x == 0;
+        auto look = [&](int b, int2 &r, int &T) {  // blocks of request b
+            r = make_int2(0, 0);
+            T = 0;
+            if (b >= a.batch) return 0;
+            r = request_rows(a, b);
+            const int raw_T = __ldg(a.seq_lens + b);
+            T = clamp_to(raw_T, a.t_max);
+            if (flags) {
+                const int raw_s = __ldg(a.query_start + b), raw_e = __ldg(a.query_start + b + 1);
+                if (raw_s < 0 || raw_e < raw_s || raw_e > a.tokens || raw_T != T || r.y > raw_T)
+                    record_error(a.status, DIFFQKV_ERR_DEVICE_SEQLEN);
+            }
+            return (r.y + kRows - 1) / kRows;
+        };
+        auto found = [&](int b, int block, const int2 &r, int T, int pieces, int piece, int record) {
+            ms.found[0] = b;
+            ms.found[1] = block;
+            ms.found[2] = r.x;
+            ms.found[3] = r.y;
+            ms.found[4] = T;
+            ms.found[5] = pieces;
+            ms.found[6] = piece;
+            ms.found[7] = record;
+        };
+        const int want = (int)(blockIdx.x / a.n_q);
+        if (lane == 0) ms.found[0] = -1;
+        __syncwarp();
+        int2 r;
+        int T;
+        if (a.batch <= kCutBatch) {
+            const int n = look(lane, r, T);
+            const int s = a.max_pieces > 0 ? cut_units(a, n, r.y, T, lane) : 1;  // pieces of each of this request's blocks
+            const int mine = n * s;
+            int before = 0, records = 0;
+            for (int j = 0; j < a.batch; ++j) {
+                const int Tj = __shfl_sync(0xffffffffu, T, j), nj = __shfl_sync(0xffffffffu, mine, j);
+                const int cj = __shfl_sync(0xffffffffu, s > 1 ? mine : 0, j);
+                if (Tj > T || (Tj == T && j > lane)) {
+                    before += nj;
+                    records += cj;
+                }
+            }
+            if (want >= before && want < before + mine) {
+                const int x = want - before, block = x / s;
+                found(lane, n - 1 - block, r, T, s, x - block * s, (records + block * s) * a.n_q);
+            }
+        } else {
+            int after = 0;  // blocks of the requests behind this group of 32
+            for (int base = (a.batch - 1) / 32 * 32; base >= 0; base -= 32) {
+                const int n = look(base + lane, r, T);
+                int incl = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_down_sync(0xffffffffu, incl, off);
+                    if (lane + off < 32) incl += y;
+                }
+                const int before = after + incl - n;
+                if (want >= before && want < before + n) found(base + lane, n - 1 - (want - before), r, T, 1, 0, 0);
+                after += __shfl_sync(0xffffffffu, incl, 0);
+            }
+        }
+    }
+    __syncthreads();
+    const int b = ms.found[0];
+    if (b < 0) return;
+    const int h = blockIdx.x % a.n_q;
+    const int row0 = ms.found[1] * kRows, n_rows = ms.found[3], T = ms.found[4];
+    const int first = T - n_rows;  // position of the request's first row
+    const int q0 = ms.found[2] + row0;
+    const int kh = h / (a.n_q / a.n_k), vh = h / (a.n_q / a.n_v);
+
+    int n_kv[QT];  // K/V tiles that a query tile's rows see
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int rows = min(n_rows - row0 - t * BM, BM);
+        const int last = first + row0 + t * BM + rows - 1;
+        n_kv[t] = uniform(rows > 0 && last >= 0 ? last / BN + 1 : 0);
+    }
+    const int n_all = max(n_kv[0], n_kv[1]);
+    const int chunk = uniform((n_all + ms.found[5] - 1) / ms.found[5]), piece = uniform(ms.found[6]);
+    const int n0 = piece * chunk, n1 = min(n_all, n0 + chunk);
+    // this unit's records and counter, piece by piece; 0 where it is whole
+    const int pieces = chunk > 0 ? (n_all + chunk - 1) / chunk : 1, record = ms.found[7] + h * ms.found[5];
+    if (n_all == 0 || n0 >= n1) {
+        if (n_all == 0 && piece == 0)  // rows without a position
+            for (int e = tid; e < min(n_rows - row0, kRows) * (DV / 8); e += kThreads)
+                *reinterpret_cast<uint4 *>(a.out + ((size_t)(q0 + e / (DV / 8)) * a.n_q + h) * DV + e % (DV / 8) * 8) =
+                    make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int end[QT] = {min(n_kv[0], n1), min(n_kv[1], n1)};
+
     if (warp == kMmaWarp) {
         tmem_alloc(&ms.tmem_slot, 512);
         tmem_relinquish();
@@ -513,37 +617,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rr = row0 + t * BM + r;        // row of the request
         const int i = first + rr;                // its position
         const bool live = rr < n_rows;
-        const size_t qrow = ((size_t)(q0 + t * BM + r) * a.n_q + h);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         constexpr int HV = DV / 2;               // this thread's columns of O
         const uint32_t t_o = tmem + T_O + (uint32_t)(t * DV + half * HV) + lane_base;
         float sc_row;  // scale * log2(e) * 2^(the query's exponent)
         {
-            // the row in f16, its largest element brought into [2^14, 2^15) by a power of two
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow * DK);
-            uint8_t *dst = smem + t * C::Q_BYTES + r * 128;
-            const bool have = live && in_bounds((long long)qrow, (long long)a.tokens * a.n_q, a.status);
-            uint32_t m = 0;
+            // The rows in f16, a row's largest element brought into [2^14, 2^15) by a power of two.  Of the 32 rows of two
+            // warps each takes 16, a row's 16-byte pieces side by side: a thread to a row would touch 32 lines a load.
+            constexpr int LPR = DK / 8, RPI = 32 / LPR, NI = 16 / RPI;
+            const int c = lane % LPR, rb = (warp & 3) * 32 + half * 16 + lane / LPR;
+            uint4 x[NI];
 #pragma unroll
-            for (int c = 0; c < DK / 8; ++c) {
-                const uint4 x = have ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
-                m = __vmaxu2(__vmaxu2(m, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+            for (int k = 0; k < NI; ++k) {
+                const size_t g = (size_t)(q0 + t * BM + rb + k * RPI) * a.n_q + h;
+                x[k] = row0 + t * BM + rb + k * RPI < n_rows && in_bounds((long long)g, (long long)a.tokens * a.n_q, a.status)
+                           ? __ldg(reinterpret_cast<const uint4 *>(a.q + g * DK) + c)
+                           : make_uint4(0, 0, 0, 0);
             }
-            m = max(m & 0xffffu, m >> 16);
-            const int se = min(141 - (int)(m >> 7), 126);
-            const float f = exp2_int(se);
 #pragma unroll
-            for (int c0 = 0; c0 < DK / 16; ++c0) {
-                const int c = half * (DK / 16) + c0;
-                const uint4 x = have ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < NI; ++k) {
+                const int rq = rb + k * RPI;
+                uint32_t m = __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                                      __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+                m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+                for (int off = 1; off < LPR; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+                const float f = exp2_int(min(141 - (int)(m >> 7), 126));
                 uint4 y;
-                y.x = pack_f16x2(bf16lo(x.x) * f, bf16hi(x.x) * f);
-                y.y = pack_f16x2(bf16lo(x.y) * f, bf16hi(x.y) * f);
-                y.z = pack_f16x2(bf16lo(x.z) * f, bf16hi(x.z) * f);
-                y.w = pack_f16x2(bf16lo(x.w) * f, bf16hi(x.w) * f);
-                *reinterpret_cast<uint4 *>(dst + (c >> 3) * (BM * 128) + ((c & 7) ^ (r & 7)) * 16) = y;
+                y.x = pack_f16x2(bf16lo(x[k].x) * f, bf16hi(x[k].x) * f);
+                y.y = pack_f16x2(bf16lo(x[k].y) * f, bf16hi(x[k].y) * f);
+                y.z = pack_f16x2(bf16lo(x[k].z) * f, bf16hi(x[k].z) * f);
+                y.w = pack_f16x2(bf16lo(x[k].w) * f, bf16hi(x[k].w) * f);
+                *reinterpret_cast<uint4 *>(smem + t * C::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 + ((c & 7) ^ (rq & 7)) * 16) = y;
+                if (c == 0) ms.row_s[t][0][rq] = __uint_as_float(m);
             }
+            named_barrier(bar, 64);
+            const uint32_t m = __float_as_uint(ms.row_s[t][0][r]);
+            const int se = min(141 - (int)(m >> 7), 126);
+            named_barrier(bar, 64);
             // a row with infinities or NaN has no scale: its scores become NaN
             sc_row = m >= 0x7f80u ? __int_as_float(0x7fffffff) : a.scale_log2 * exp2_int(-se);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -653,50 +764,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_barrier(bar, 64);
         l += ms.row_s[t][1 - half][r];
         const float o_scale = exp2f((float)v_run);  // (l carries the weights' 2^7 as O does)
-        if (a.splits == 1) {
-            const float inv_l = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row without a position: zeros)
-            __nv_bfloat16 *orow = a.out + qrow * DV + half * HV;
-            const bool put = live && in_bounds((long long)qrow, (long long)a.tokens * a.n_q, a.status);
+        // A whole unit: the rows, divided by their sums.  Otherwise this piece's record: O relative to m, four columns of all
+        // rows after another, then (m, l) of the rows.
+        const bool whole = pieces == 1;
+        const bool some = done > 0 && i >= 0 && n0 * BN <= i;  // the row sees a position of this piece
+        const float inv_l = !whole ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
+        // Whole rows leave through the pair's 32 rows of Q, free now, 32 columns at a time, so that a warp's store covers whole
+        // sectors of few rows (a thread to a row touches 32 lines a store).
+        uint4 *rec = reinterpret_cast<uint4 *>(a.partials + (size_t)(record + piece) * C::REC) + half * (HV / 4) * kRows + t * BM + r;
+        uint8_t *stage = smem + t * C::Q_BYTES + (warp & 3) * 4096 + half * 2048;
 #pragma unroll 1
-            for (int c = 0; c < HV; c += 16) {
-                uint32_t y[16];
-                if (done > 0) {
-                    tmem_ld_cols<16>(t_o + c, y);
-                    tmem_wait_ld();
-                }
-                if (put) {
+        for (int c = 0; c < HV; c += 16) {
+            uint32_t y[16];
+            if (done > 0) {
+                tmem_ld_cols<16>(t_o + c, y);
+                tmem_wait_ld();
+            }
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        float z[8];
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(some ? __uint_as_float(y[e]) * inv_l * o_scale : 0.f);
+            if (whole) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            z[j] = done > 0 && i >= 0 ? __uint_as_float(y[e + j]) * inv_l * o_scale : 0.f;
-                        *reinterpret_cast<uint4 *>(orow + c + e) =
-                            make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                                       pack_bf16x2(z[6], z[7]));
+                for (int e = 0; e < 16; e += 2)
+                    y[e >> 1] = pack_bf16x2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+                const int ch = c >> 3 & 2, sw = lane >> 1 & 3;  // 16-byte pieces of a 64-byte row, permuted
+                *reinterpret_cast<uint4 *>(stage + lane * 64 + (ch ^ sw) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(stage + lane * 64 + ((ch + 1) ^ sw) * 16) = make_uint4(y[4], y[5], y[6], y[7]);
+                if (ch == 2) {
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int ro = k * 8 + (lane >> 2), rg = t * BM + (warp & 3) * 32 + ro;
+                        const size_t g = (size_t)(q0 + rg) * a.n_q + h;
+                        if (row0 + rg < n_rows && in_bounds((long long)g, (long long)a.tokens * a.n_q, a.status))
+                            *reinterpret_cast<uint4 *>(a.out + g * DV + half * HV + (c - 16) + (lane & 3) * 8) =
+                                lds128(stage + ro * 64 + ((lane & 3) ^ (ro >> 1 & 3)) * 16);
                     }
+                    __syncwarp();
                 }
-            }
-        } else {
-            // this split's partial: m, l and O relative to m, the record's rows in a row of d_v + 2 columns
-            float *rec = a.partials + ((size_t)(blockIdx.x * a.splits + blockIdx.y) * kRows + t * BM + r) * (DV + 2);
-            const bool some = done > 0 && i >= 0 && n0 * BN <= i;  // the row sees a position of this split
-#pragma unroll 1
-            for (int c = 0; c < HV; c += 16) {
-                uint32_t y[16];
-                if (done > 0) {
-                    tmem_ld_cols<16>(t_o + c, y);
-                    tmem_wait_ld();
-                }
-                if (live)
+            } else if (live) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2)
-                        __stcg(reinterpret_cast<float2 *>(rec + half * HV + c + e),
-                               some ? make_float2(__uint_as_float(y[e]) * o_scale, __uint_as_float(y[e + 1]) * o_scale)
-                                    : make_float2(0.f, 0.f));
+                for (int e = 0; e < 16; e += 4, rec += kRows) __stcg(rec, make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]));
             }
+        }
+        if (!whole) {
             if (live && half == 0)
-                __stcg(reinterpret_cast<float2 *>(rec + DV), some ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f));
+                __stcg(reinterpret_cast<float2 *>(a.partials + (size_t)(record + piece) * C::REC + (size_t)DV * kRows) + t * BM + r,
+                       some ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f));
             __threadfence();
         }
     }
@@ -706,38 +819,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (a.splits == 1) return;
+    if (pieces == 1) return;
 
-    // ---- split units: the last CTA merges the partials
-    const int used = (n_all + chunk - 1) / chunk;
+    // ---- a cut unit: the last of its CTAs merges the records
     if (tid == 0) {
         __threadfence();
-        ms.last_flag = atomicAdd(a.counters + blockIdx.x, 1u) == (unsigned)(used - 1);
+        ms.last_flag = atomicAdd(a.counters + record, 1u) == (unsigned)(pieces - 1);
     }
     __syncthreads();
     if (!*(volatile int *)&ms.last_flag) return;
     __threadfence();
     const int rows = min(n_rows - row0, kRows);
-    for (int e = tid; e < rows * (DV / 2); e += kThreads) {
-        const int r = e / (DV / 2), d = e % (DV / 2) * 2;
-        const float *base = a.partials + ((size_t)blockIdx.x * a.splits * kRows + r) * (DV + 2);
-        const size_t step = (size_t)kRows * (DV + 2);
-        float M = -INFINITY;
-        for (int s = 0; s < used; ++s) M = fmaxf(M, __ldcg(base + s * step + DV));
-        float L = 0.f, x = 0.f, y = 0.f;
-        for (int s = 0; s < used; ++s) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(base + s * step + DV));
-            if (ml.x == -INFINITY) continue;  // nothing of this split is seen by the row
-            const float2 o = __ldcg(reinterpret_cast<const float2 *>(base + s * step + d));
-            const float f = fast_exp2(ml.x - M);
-            L = fmaf(f, ml.y, L);
-            x = fmaf(f, o.x, x);
-            y = fmaf(f, o.y, y);
-        }
-        const float inv = M == -INFINITY ? 0.f : 1.f / L;
-        *reinterpret_cast<uint32_t *>(a.out + ((size_t)(q0 + r) * a.n_q + h) * DV + d) = pack_bf16x2(x * inv, y * inv);
-    }
-    if (tid == 0) a.counters[blockIdx.x] = 0u;
+    if (rows * (DV / 4) <= kThreads) merge_pieces<DV, 1, 8>(a, record, pieces, q0, rows, h, tid);
+    else merge_pieces<DV, 4, 2>(a, record, pieces, q0, rows, h, tid);
+    if (tid == 0) a.counters[record] = 0u;
 }
 
 // ------------------------------------------------------------------ host side
@@ -824,13 +919,18 @@ diffqkv_status_t prefill_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_c
     a.scale_blocks = (long long)cache->num_pages * (P / cache->scale_block);
     a.scale_log2 = (float)((double)d->scale * 1.4426950408889634);
     a.wait_limit_ns = kWaitLimitNs;
-    // units for fewer than half of the SMs: cut their K/V tiles
-    a.splits = units * 2 <= dev.num_sms ? (int)(std::min(dev.num_sms, kSlots) / units) : 1;
+    // Units for at most half of the SMs are cut so that every SM has a piece (on the device, which alone knows the lengths:
+    // `fewest` and `units` are what their number can be).  Pieces for more than one wave measured no better than whole
+    // units, longest first: 409 against 406 us for 384 units of 78 to 250 tiles.
+    const long long fewest = ((long long)tokens + kRows - 1) / kRows * d->n_q;
+    const int ctas = std::min(dev.num_sms, kSlots);
+    a.max_pieces = d->batch <= kCutBatch && fewest * 2 <= ctas ? ctas : 0;
+    const unsigned grid = (unsigned)std::max(units, (long long)a.max_pieces);
     int smem = 0;
     PreFn fn = d->d_k == 64 ? (d->d_v == 64 ? plan<64, 64>(&smem) : plan<64, 128>(&smem))
                             : (d->d_v == 64 ? plan<128, 64>(&smem) : plan<128, 128>(&smem));
     if (ensure_dynamic_smem((const void *)fn, smem) != DIFFQKV_OK) return DIFFQKV_ERR_CUDA;
-    fn<<<dim3((unsigned)units, (unsigned)a.splits), kThreads, smem, stream>>>(tm_k, tm_v, a);
+    fn<<<grid, kThreads, smem, stream>>>(tm_k, tm_v, a);
     return cudaGetLastError() == cudaSuccess ? DIFFQKV_OK : DIFFQKV_ERR_CUDA;
 }
 

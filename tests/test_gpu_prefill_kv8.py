@@ -77,6 +77,15 @@ def test_few_rows_over_a_long_context_are_split(cuda_device, rows, length):
     _case(Shape(2, 2, 1, 128, 128), [rows], [length // 2], 64, 64, cuda_device, seed=rows + 1)
 
 
+@pytest.mark.parametrize("rows,lens", [([256, 5, 0, 130], [4100, 7000, 64, 131]), ([600], [600]), ([600], [5000]),
+                                       ([1] * 32, [65 + 40 * i for i in range(32)]),
+                                       ([1] * 33, [65 + 40 * i for i in range(33)]), ([0, 3], [0, 2000])], ids=str)
+def test_ragged_batches_are_cut(cuda_device, rows, lens):
+    """Few heads, so that units are cut into many pieces: blocks with fewer tiles than pieces, requests of very different
+    lengths, empty ones."""
+    _case(Shape(4, 1, 4, 64, 128), rows, lens, 16, 16, cuda_device)
+
+
 @pytest.mark.parametrize("spread", [6, 10])
 def test_scales_far_apart(cuda_device, spread):
     _case(wl.DIFFQKV, [90], [900], 16, 16, cuda_device, seed=4, spread=spread, q_gain=2.0 ** -spread)
