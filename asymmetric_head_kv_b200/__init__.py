@@ -10,6 +10,7 @@ torch provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -394,6 +395,12 @@ def prefill_causal_paged(q, k_pages, v_pages, block_table, prefix_len: int, *, s
     return out
 
 
+def _on(stream: Optional[torch.cuda.Stream]):
+    """Context for what a call allocates itself: on its stream, so that a buffer is neither filled nor handed on by
+    another one."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
              page_size: int, num_pages: int, query_start: Optional[torch.Tensor] = None,
              slot_map: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
@@ -408,18 +415,20 @@ def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
     give them, or ``capacity`` (rows of the step's token buffer) to have them allocated.  A step that does not fit
     ``capacity`` or ``free_pages`` is dropped as a whole and flagged (``diffqkv_page_map``)."""
     i32 = torch.int32
-    if slot_map is None:
-        if capacity is None:
-            raise ValueError("give slot_map, or capacity")
-        slot_map = torch.empty(int(capacity), dtype=i32, device=seq_lens.device)
-        if positions is None:
-            positions = torch.empty_like(slot_map)
-    if query_start is None:
-        query_start = torch.empty(seq_lens.numel() + 1, dtype=i32, device=seq_lens.device)
-    if total_lens is None:
-        total_lens = torch.empty(seq_lens.numel(), dtype=i32, device=seq_lens.device)
-    if pages_used is None:
-        pages_used = torch.empty(1, dtype=i32, device=seq_lens.device)
+    if slot_map is None or query_start is None or total_lens is None or pages_used is None:
+        with _on(stream):
+            if slot_map is None:
+                if capacity is None:
+                    raise ValueError("give slot_map, or capacity")
+                slot_map = torch.empty(int(capacity), dtype=i32, device=seq_lens.device)
+                if positions is None:
+                    positions = torch.empty_like(slot_map)
+            if query_start is None:
+                query_start = torch.empty(seq_lens.numel() + 1, dtype=i32, device=seq_lens.device)
+            if total_lens is None:
+                total_lens = torch.empty(seq_lens.numel(), dtype=i32, device=seq_lens.device)
+            if pages_used is None:
+                pages_used = torch.empty(1, dtype=i32, device=seq_lens.device)
     st = serving().page_map(seq_lens, new_lens, block_table, free_pages, page_size, num_pages, query_start, slot_map,
                             positions, total_lens, pages_used, status, stream)
     check(st, "diffqkv_page_map")
@@ -466,10 +475,13 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     """:func:`decode` over an 8-bit paged cache: e4m3 pools k_pages [num_pages, page_size, n_k, d_k] and v_pages
     [num_pages, page_size, n_v, d_v], scale bytes [num_pages, page_size // scale_block, heads], block_table int32
     [B, max_blocks], seq_lens int32 [B].  Returns bf16 [B, n_q, d_v]."""
-    if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], v_pages.shape[3]), dtype=torch.bfloat16, device=q.device)
-    if workspace is None:
-        workspace = decode_workspace(_kv8_dims(q, q.shape[0], k_pages, v_pages), device=q.device)
+    if out is None or workspace is None:
+        dims = _kv8_dims(q, q.shape[0], k_pages, v_pages)
+        with _on(stream):
+            if out is None:
+                out = torch.empty((q.shape[0], q.shape[1], v_pages.shape[3]), dtype=torch.bfloat16, device=q.device)
+            if workspace is None:
+                workspace = decode_workspace(dims, device=q.device)
     st = serving().decode_paged_kv8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, scale,
                                     0 if max_seq_len is None else max_seq_len, out, workspace, stream)
     check(st, "diffqkv_decode_paged_kv8")
@@ -493,10 +505,13 @@ def prefill_paged_kv8(q: torch.Tensor, query_start: torch.Tensor, k_pages: torch
     owning rows query_start[b] .. query_start[b + 1] - 1 (int32 [B + 1], as :func:`page_map` writes it) at the last
     positions of its seq_lens[b] (int32 [B], the new rows included and stored).  Returns bf16 [tokens, n_q, d_v]; rows
     behind query_start[B] are not written."""
-    if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], v_pages.shape[3]), dtype=torch.bfloat16, device=q.device)
-    if workspace is None:
-        workspace = prefill_paged_kv8_workspace(_kv8_dims(q, block_table.shape[0], k_pages, v_pages), q.device)
+    if out is None or workspace is None:
+        dims = _kv8_dims(q, block_table.shape[0], k_pages, v_pages)
+        with _on(stream):
+            if out is None:
+                out = torch.empty((q.shape[0], q.shape[1], v_pages.shape[3]), dtype=torch.bfloat16, device=q.device)
+            if workspace is None:
+                workspace = prefill_paged_kv8_workspace(dims, q.device)
     st = serving().prefill_paged_kv8(q, query_start, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, scale, out,
                                      workspace, stream)
     check(st, "diffqkv_prefill_paged_kv8")

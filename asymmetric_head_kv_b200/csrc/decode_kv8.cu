@@ -26,9 +26,16 @@
 //  * work split, ragged batches, ring of TMA stages, partials and the combine by the last CTA of a unit are those of
 //    decode.cu.  K tiles and V head tiles have rings of their own (a V slot is one head of one tile: any number of V
 //    heads per K head fits), the K tile of the next step is requested before the V tiles of this one.
-//  * four warps fetch the tiles' scale bytes (through the block table) four tiles ahead.
+//  * three warps fetch the tiles' scale bytes (through the block table), each a tile of three, up to three ahead.
 //  * rows of a sequence's last tile behind its end are zeroed in shared memory before the MMA reads them: their weights
 //    are zero, but the codes there may be NaN.
+//  * MMA, commit and TMA are issued by an elected lane (kv8.cuh): behind a test of the lane index the MMA warp alone
+//    took longer than a tile's bytes.
+// 16 sequences of 32768, 4 K heads of 64 and 16 V heads of 128: 201 us from pages of 16, 6.0 TB/s, 0.93 of the measured
+// copy bandwidth; 195 us from pages of 64.  32 query heads over 4 + 16 heads of 64: 3.3 TB/s, 16 + 16 heads of 128: 5.6 TB/s;
+// the fewer bytes a tile has for its heads, the more the softmax warps' time shows (about 3400 clocks a tile and CTA, two
+// CTAs an SM): exponentials, the e4m3 terms (a conversion of two values takes 4 clocks) and three shared-memory barriers.
+// One sequence of 512: 9.4 us, a chain of launch, table, TMA, two MMAs, partials and merge.
 #include <math.h>
 
 #include <algorithm>
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_wait_bounded(&ms.mma_done, 0, a.wait_limit_ns, nullptr, a.status);
         }
     } else if (warp >= kScaleWarp0) {
-        // ======================= scale bytes: warp j fetches those of tiles j, j + 4, ... into slot j
+        // ======================= scale bytes: warp j fetches those of tiles j, j + kScaleWarps, ... into slot j
         const int j = warp - kScaleWarp0;
         int8_t *ke = reinterpret_cast<int8_t *>(sc_s + j * a.sc_bytes);  // [128] K exponents, then [vpg][128] of V
         int8_t *ve = ke + kTT;

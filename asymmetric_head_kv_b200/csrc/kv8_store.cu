@@ -18,12 +18,17 @@
 // owns a (run, head), so the block's maximum needs no atomics and no second launch; the rows stay in registers between the
 // maximum and the rounding (longer runs are read twice).  The first rows are requested together with the slots,
 // before it is known which run they belong to: most often they are the ones.
-// Two shapes of group, by the rows a run can have:
-//  * blocks of more than kRowBlock positions, and steps of few tokens: `share` warps, as many as hold a whole block in
-//    registers (16 rows of 128 or 32 of 64 a warp), over the runs that begin in the CTA's chunk of tokens; the maximum crosses
-//    a warp in one redux and the warps through shared memory;
-//  * smaller blocks: the 8 or 16 lanes of one row, every (token, head) has a group and those whose token does not begin
-//    a run have nothing to do.
+// Shapes of group, by the rows a run can have (4 heads of 64 and 16 of 128 unless stated, inputs beyond L2):
+//  * `share` warps over the runs that begin in the CTA's chunk of tokens: one warp (CTAs of four) where it holds a block in
+//    registers (16 rows of 128 or 32 of 64), otherwise as many as do (CTAs of eight); the maximum crosses a warp in one
+//    redux and the warps through shared memory.  16384 tokens in blocks of 16: 25.5 us, 4.4 TB/s, 0.69 of the copy rate;
+//    CTAs of eight for one warp: 27.7.  Blocks of 64, 3704 tokens of 16 + 16 heads of 128: 17.3 us shared, 21.0 with one
+//    warp; 128: 50 against 54 (16384 tokens); blocks of 64 with 16384 tokens would be 36 against 38 the other way.
+//    What keeps it from the copy rate: the CTAs' start (slots, run, rows: two loads deep) is not hidden by others' work.
+//  * a chunk of one token for up to kFewTokens, so that a decode step's heads and requests spread over the SMs: 16 tokens
+//    3.5 us against 4.9 with chunks of 16, 256 tokens 4.5 against 5.4, but 512 tokens 5.9 against 5.2.
+//  * blocks of up to kRowBlock positions in larger steps: the 8 or 16 lanes of one row take kRowVec tokens and the runs
+//    that begin there.  16384 tokens: blocks of one 68 us (a warp a run: 186), of four 36 us (a warp: 58).
 #include <algorithm>
 #include <type_traits>
 
@@ -38,7 +43,8 @@ constexpr int kStoreWarps = 8;
 constexpr int kRunVec = 8, kRowVec = 4;  // 16-byte loads a lane keeps, by shape of group
 constexpr int kMaxTokens = 32; // tokens whose runs one CTA may lead
 constexpr int kRowBlock = 4;   // blocks up to this size take a row's lanes
-constexpr int kFewTokens = 512;
+constexpr int kFewTokens = 256;
+constexpr int run_warps(bool shared) { return shared ? kStoreWarps : kStoreWarps / 2; }
 
 struct StoreArgs {
     const uint4 *k_new, *v_new;
@@ -185,13 +191,14 @@ __device__ __forceinline__ void store_run(const StoreArgs &a, const uint4 *x, ui
 }
 
 template <int DK, int DV, bool SHARED>
-__global__ void __launch_bounds__(kStoreWarps * 32, 3) kv8_store_runs_kernel(const StoreArgs a) {
-    __shared__ uint32_t cross[kStoreWarps];
+__global__ void __launch_bounds__(run_warps(SHARED) * 32, 24 / run_warps(SHARED)) kv8_store_runs_kernel(const StoreArgs a) {
+    constexpr int WARPS = run_warps(SHARED);
+    __shared__ uint32_t cross[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int share = SHARED ? a.share : 1;
     const int heads = a.n_k + a.n_v;
     // the (run, head)s of this warp: one head, the runs that begin in the CTA's chunk of tokens
-    const int head = blockIdx.y * (kStoreWarps / share) + warp / share, mine = warp % share;
+    const int head = blockIdx.y * (WARPS / share) + warp / share, mine = warp % share;
     const int t_begin = blockIdx.x * a.chunk;
     uint4 keep[kRunVec];
     if (!SHARED && head < heads) {  // the chunk's rows, before the slots are there
@@ -247,57 +254,79 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 3) kv8_store_runs_kernel(con
     }
 }
 
-// One group of D / 8 lanes per (token, head); blockIdx.y: K or V.
+// One group of D / 8 lanes per head and kRowVec tokens: the runs that begin among them.
 template <int D>
 __device__ __forceinline__ void store_rows(const StoreArgs &a, const uint4 *x, uint8_t *pages, uint8_t *scales, int heads,
-                                           bool flag) {
-    constexpr int LPR = D / 8;
-    const unsigned group = (blockIdx.x * (kStoreWarps * 32u) + threadIdx.x) / LPR;
-    const int t = (int)(group / (unsigned)heads), head = (int)(group - (unsigned)t * heads);
-    if (t >= a.tokens) return;
-    uint4 keep[kRowVec];
-    keep[0] = __ldg(x + (size_t)group * LPR + threadIdx.x % LPR);  // this row, before the slots are there
-    const int raw = __ldg(a.slot_map + t);
-    const int before = t > 0 ? slot_of(a, t - 1) : -1;
-    int next = t + 1 < a.tokens ? slot_of(a, t + 1) : -1;
-    if (raw >= a.slots && flag && head == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
-    if (raw < 0 || raw >= a.slots) return;
-    const int blk = block_of(a, raw);
-    if (before >= 0 && block_of(a, before) == blk) return;
-    int len = 1, low = raw - blk * a.sb;
-    while (next >= 0 && block_of(a, next) == blk) {
-        low = min(low, next - blk * a.sb);
-        ++len;
-        next = t + len < a.tokens ? slot_of(a, t + len) : -1;
+                                           unsigned cta, bool flag) {
+    constexpr int LPR = D / 8, VEC = kRowVec;
+    const unsigned group = (cta * (kStoreWarps * 32u) + threadIdx.x) / LPR;
+    const int t0 = (int)(group / (unsigned)heads) * VEC, head = (int)(group % (unsigned)heads);
+    if (t0 >= a.tokens) return;
+    auto row = [&](int t) { return __ldg(x + ((size_t)t * heads + head) * LPR + threadIdx.x % LPR); };
+    uint4 rows[VEC];  // before the slots are there
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        if (t0 + v < a.tokens) rows[v] = row(t0 + v);
+    int slot[VEC], blk[VEC + 2];  // blk[v + 1]: block of token t0 + v
+#pragma unroll
+    for (int v = -1; v <= VEC; ++v) {
+        const int t = t0 + v, raw = t >= 0 && t < a.tokens ? __ldg(a.slot_map + t) : -1;
+        if (v >= 0 && v < VEC) {
+            slot[v] = raw;
+            if (raw >= a.slots && flag && head == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+        }
+        blk[v + 1] = raw >= 0 && raw < a.slots ? block_of(a, raw) : -1;
     }
 #pragma unroll
-    for (int v = 1; v < kRowVec; ++v)
-        if (v < len) keep[v] = __ldg(x + ((size_t)(t + v) * heads + head) * LPR + threadIdx.x % LPR);
-    store_run<D, LPR>(a, x, pages, scales, heads, head, t, len, blk, low, (int)threadIdx.x % LPR, keep, true);
+    for (int v = 0; v < VEC; ++v) {
+        const int b = blk[v + 1];
+        if (b < 0 || blk[v] == b) continue;
+        int len = 1, low = slot[v] - b * a.sb;
+#pragma unroll
+        for (int w = v + 1; w < VEC; ++w)
+            if (len == w - v && blk[w + 1] == b) {
+                low = min(low, slot[w] - b * a.sb);
+                ++len;
+            }
+        if (len == VEC - v && blk[VEC + 1] == b)  // on behind these tokens
+            for (int t = t0 + VEC, s; t < a.tokens && (s = slot_of(a, t)) >= 0 && block_of(a, s) == b; ++t) {
+                low = min(low, s - b * a.sb);
+                ++len;
+            }
+        uint4 keep[VEC];
+#pragma unroll
+        for (int w = 0; w < VEC; ++w)
+            if (w < len) keep[w] = v + w < VEC ? rows[v + w] : row(t0 + v + w);
+        store_run<D, LPR>(a, x, pages, scales, heads, head, t0 + v, len, b, low, (int)threadIdx.x % LPR, keep, true);
+    }
 }
 
+// The first k_ctas CTAs: K, the others: V.
 template <int DK, int DV>
-__global__ void __launch_bounds__(kStoreWarps * 32) kv8_store_rows_kernel(const StoreArgs a) {
-    if (blockIdx.y == 0)
-        store_rows<DK>(a, a.k_new, a.k_pages, a.k_scales, a.n_k, true);
+__global__ void __launch_bounds__(kStoreWarps * 32) kv8_store_rows_kernel(const StoreArgs a, unsigned k_ctas) {
+    if (blockIdx.x < k_ctas)
+        store_rows<DK>(a, a.k_new, a.k_pages, a.k_scales, a.n_k, blockIdx.x, true);
     else
-        store_rows<DV>(a, a.v_new, a.v_pages, a.v_scales, a.n_v, false);
+        store_rows<DV>(a, a.v_new, a.v_pages, a.v_scales, a.n_v, blockIdx.x - k_ctas, false);
 }
 
 template <int DK, int DV>
 void store_launch(const StoreArgs &a, cudaStream_t stream) {
     if (a.sb <= kRowBlock && a.tokens > kFewTokens) {
-        const long long k = (long long)a.tokens * a.n_k * (DK / 8), v = (long long)a.tokens * a.n_v * (DV / 8);
-        const long long ctas = (std::max(k, v) + kStoreWarps * 32 - 1) / (kStoreWarps * 32);
-        kv8_store_rows_kernel<DK, DV><<<dim3((unsigned)ctas, 2), kStoreWarps * 32, 0, stream>>>(a);
+        auto ctas = [&](int heads, int d) {
+            const long long threads = ((long long)a.tokens + kRowVec - 1) / kRowVec * heads * (d / 8);
+            return (unsigned)((threads + kStoreWarps * 32 - 1) / (kStoreWarps * 32));
+        };
+        const unsigned k = ctas(a.n_k, DK), v = ctas(a.n_v, DV);
+        kv8_store_rows_kernel<DK, DV><<<k + v, kStoreWarps * 32, 0, stream>>>(a, k);
         return;
     }
-    const int per_cta = kStoreWarps / a.share;
+    const int per_cta = run_warps(a.share > 1) / a.share;
     const dim3 grid((a.tokens + a.chunk - 1) / a.chunk, (a.n_k + a.n_v + per_cta - 1) / per_cta);
     if (a.share > 1)
-        kv8_store_runs_kernel<DK, DV, true><<<grid, kStoreWarps * 32, 0, stream>>>(a);
+        kv8_store_runs_kernel<DK, DV, true><<<grid, run_warps(true) * 32, 0, stream>>>(a);
     else
-        kv8_store_runs_kernel<DK, DV, false><<<grid, kStoreWarps * 32, 0, stream>>>(a);
+        kv8_store_runs_kernel<DK, DV, false><<<grid, run_warps(false) * 32, 0, stream>>>(a);
 }
 
 diffqkv_status_t kv8_store_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cache_t *c, const void *k_new,

@@ -12,9 +12,12 @@
 // shared memory, and a token or page finds its request by a binary search over the runs and a walk
 // inside one.  No CTA reads what another writes: the slot of a token in a new page comes from the
 // free list, not from the table entry.
-// Up to kManyThreads requests a thread has one request, and what the tokens need of it (its length, its pages, the page that
-// it fills first, and the head of the free list) is fetched beside the sums and kept in shared memory: the map of a decode
-// step then has two dependent global loads in a row instead of five.
+// Up to kManyThreads requests a thread has one request (ONE), and what the tokens need of it (its length, its pages, the
+// page that it fills first, and the head of the free list) is fetched beside the sums and kept in shared memory: the map of a
+// decode step then has two dependent global loads in a row instead of five.  64 requests with a token each 4.4 us against
+// 4.8 without, 512 requests 5.6 against 6.1; 1024 prompts of up to 1023 tokens 7.35 against 7.25.
+// CTAs of kFewThreads threads up to as many requests, of kManyThreads beyond: 256 requests of up to 127 tokens 4.8 us against
+// 6.1 with the larger CTAs, 64 requests 4.4 against 4.8.
 #include "common.cuh"
 #include "internal.h"
 

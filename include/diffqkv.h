@@ -536,9 +536,9 @@ typedef struct {
  * below the lowest one written are moved to it (code * 2^(e_old - e), to nearest even:
  * exact down to the smallest normal code).  Rows above stay as they are.  Then
  * code = e4m3(x * 2^-e), to nearest even.  Infinities become +-448 * 2^e, NaN stays NaN;
- * neither takes part in a.  (Magnitudes above 448 * 2^119 become that.)  So a block is filled in the order of its rows, over as many
- * calls as one likes; the values do not depend on how a block's rows are dealt out to
- * calls beyond those roundings.
+ * neither takes part in a.  (Magnitudes above 448 * 2^119 become that.)  So a block is
+ * filled in the order of its rows, over as many calls as one likes; the values do not
+ * depend on how a block's rows are dealt out to calls beyond those roundings.
  *
  * The tokens of one scale block must be consecutive in the call (they are in the maps of
  * diffqkv_page_map, where a request's tokens are consecutive and pages belong to one
@@ -564,9 +564,10 @@ diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8
  *   out         [B, n_q, d_v]           bf16
  *
  * out[b,h] = sum_j softmax_j(scale q[b,h].k_j) v_j over the values k_j, v_j the cache
- * stands for.  The codes go to the tensor cores as they are; the query and the softmax weights
- * (times their V scales) are split into three e4m3 terms each: 12 significant bits, or 2^-28 of the
- * head's largest where that is more.  All sums, maxima and weights are fp32.  Lengths, clamping, zero rows for length 0, max_seq_len, the workspace
+ * stands for.  The codes go to the tensor cores as they are; the query and the softmax
+ * weights (times their V scales) are split into three e4m3 terms each: 12 significant
+ * bits, or 2^-28 of the head's largest where that is more.  All sums, maxima and weights
+ * are fp32.  Lengths, clamping, zero rows for length 0, max_seq_len, the workspace
  * (diffqkv_decode_workspace_size) and its error word are those of diffqkv_decode; entries
  * read, bad entries and shared pages those of diffqkv_decode_paged.
  */
@@ -596,9 +597,10 @@ size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
  * descending, and n_b > seq_lens[b] are clamped and flagged DIFFQKV_ERR_DEVICE_SEQLEN in the
  * workspace's error word; a row without a position gets zeros.  Bad table entries as in
  * diffqkv_prefill_causal_paged.  Codes and queries are converted to f16 with power-of-two
- * scales (exactly, but for blocks whose scale is 2^15 below the largest of their tile of 64 positions,
- * for K, or of the sequence so far, for V), products are summed in fp32, and softmax weights are rounded
- * to f16 for the second product.  A NaN in a stored V row can also reach rows up to 255 before it.
+ * scales (exactly, but for blocks whose scale is 2^15 below the largest of their tile of
+ * 64 positions, for K, or of the sequence so far, for V), products are summed in fp32, and
+ * softmax weights are rounded to f16 for the second product.  A NaN in a stored V row can
+ * also reach rows up to 255 before it (a weight of zero times NaN).
  * tokens >= 1.  workspace as above.
  */
 diffqkv_status_t diffqkv_prefill_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
@@ -614,16 +616,16 @@ diffqkv_status_t diffqkv_prefill_paged_kv8(const diffqkv_dims_t *dims, const dif
 /* Synchronises `stream`, returns (in *device_status) the first device-side
  * error recorded in the workspace's error word since the last read
  * (DIFFQKV_OK if none), and clears that word only.  For the workspaces of
- * diffqkv_decode (and its variants) and diffqkv_decode_topv; workspace_bytes
- * >= 256, 16-byte aligned.  The return value reports failures of the query. */
+ * diffqkv_decode (and its variants), diffqkv_decode_topv and
+ * diffqkv_prefill_paged_kv8; workspace_bytes >= 256, 16-byte aligned.  The return value reports failures of the query. */
 diffqkv_status_t diffqkv_workspace_status(void *workspace, size_t workspace_bytes, diffqkv_stream_t stream,
                                           int32_t *device_status);
 
 /* Synchronises `stream`, returns (in *device_status) the first device-side
  * error recorded in the current device's word since the last read (DIFFQKV_OK
  * if none), and clears it.  Only calls without a word of their own report
- * there: diffqkv_prefill_causal / _prefix (and _ex given NULL),
- * diffqkv_decode_noalloc and diffqkv_selftest_wait_timeout.  The return value
+ * there: diffqkv_prefill_causal / _prefix, the calls that take a word where
+ * it is NULL, diffqkv_decode_noalloc and diffqkv_selftest_wait_timeout.  The return value
  * reports failures of the query. */
 diffqkv_status_t diffqkv_get_device_status(diffqkv_stream_t stream, int32_t *device_status);
 

@@ -1,0 +1,53 @@
+"""What the serving calls allocate themselves belongs to the stream they run on: a call on a side stream neither waits
+for, nor races with, the current stream's work on the same allocator pool."""
+import pytest
+import torch
+
+import asymmetric_head_kv_b200 as ak
+from kv8_inputs import pools, queries, tables
+from workloads import Shape
+
+pytestmark = pytest.mark.gpu
+
+
+def _behind_other_work(call, dev):
+    """Runs call(stream) on a side stream while the current stream holds freed, non-zero memory and is busy."""
+    side = torch.cuda.Stream(device=dev)
+    torch.cuda.synchronize()
+    dirty = [torch.full((n,), 0x5A, dtype=torch.uint8, device=dev) for n in (1 << 16, 1 << 20, 1 << 23, 1 << 25)]
+    torch.cuda._sleep(40_000_000)  # some 20 ms
+    del dirty
+    out = call(side)
+    side.synchronize()
+    busy = not torch.cuda.current_stream(dev).query()
+    out = [t.clone() for t in out]
+    torch.cuda.synchronize()
+    return out, busy
+
+
+def test_buffers_of_a_call_belong_to_its_stream(cuda_device):
+    dev, shape, lens = cuda_device, Shape(4, 1, 4, 64, 128), [4000, 900]
+    num, table = tables(lens, 16, 250, 1)
+    p = [t.to(dev) for t in pools(num, 16, 16, shape, 1)]
+    td, ld = table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
+    q, rows = queries(2, shape, 1).to(dev), queries(40, shape, 2).to(dev)
+    start = torch.tensor([0, 33, 40], dtype=torch.int32, device=dev)
+    free = torch.arange(num, dtype=torch.int32, device=dev)
+    ones = torch.ones_like(ld)
+
+    def decode(s):
+        return [ak.decode_paged_kv8(q, *p, td, ld, stream=s)]
+
+    def prefill(s):
+        return [ak.prefill_paged_kv8(rows, start, *p, td, ld, stream=s)]
+
+    def mapping(s):
+        return list(ak.page_map(ld, ones, td.clone() if s is None else spare, free, 16, num, capacity=7, stream=s))
+
+    for call in (decode, prefill, mapping):
+        want = [t.clone() for t in call(None)]
+        spare = td.clone()
+        got, busy = _behind_other_work(call, dev)
+        assert busy, "the side stream was to finish while the current one was busy"
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
