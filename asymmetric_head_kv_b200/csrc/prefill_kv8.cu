@@ -98,7 +98,7 @@ struct Misc {
     uint64_t q_full, s_full[QT][2], p_full[QT][2], pv_done[QT][2], mma_done;
     uint32_t k_mul[kScaleSlots][BN], v_mul[kScaleSlots][BN];  // 2^(e - e_ref) as f16 pairs, 0 behind the sequence
     int k_ref[kScaleSlots], v_ref[kScaleSlots];               // e_ref
-    int ref[3][2];                                            // the same by converted stage: K, V
+    int ref[4][2];  // the same for the softmax, tile k in slot k & 3: K, V
     float row_s[QT][2][BM];                                   // exchange between the two halves of a row
     int found[8];  // unit: request, block, q row, rows, length; its pieces, which of them, its first record
     uint32_t tmem_slot;
@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             widen_k.run(raw, dst, ms.k_mul[slot], tail);
             widen_v.run(raw + C::RAW_K, dst + C::K_BYTES, ms.v_mul[slot], tail);
             if (ct == 0) {
-                ms.ref[cs][0] = ms.k_ref[slot];
-                ms.ref[cs][1] = ms.v_ref[slot];
+                ms.ref[k & 3][0] = ms.k_ref[slot];
+                ms.ref[k & 3][1] = ms.v_ref[slot];
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -664,23 +664,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m_used = 0.f;  // log2 maximum that O and l are relative to (the same in both halves)
         float l = 0.f;       // this half's sum of the weights, 2^7 included
         int v_run = 0;       // V exponent that O is relative to
-        int cs = 0;
-        uint32_t cp = 0;
         for (int n = n0; n < end[t]; ++n) {
             const int k = n - n0;
             const uint32_t t_s = tmem + (uint32_t)(t * 2 * BN + (k & 1) * BN) + lane_base;
-            mbar_wait_bounded(&ms.cv_full[cs], cp, a.wait_limit_ns, abort_flag, a.status);
-            const int k_ref = ms.ref[cs][0], v_ref = ms.ref[cs][1];
-            if (++cs == C::STAGES) {
-                cs = 0;
-                cp ^= 1u;
-            }
-            float sc = sc_row * exp2_int(k_ref);
-            if (sc < 0x1p-126f) sc = 0x1p-126f;  // (a zero would turn masked scores into NaN)
             mbar_wait_bounded(&ms.s_full[t][k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             uint32_t x[32];
             tmem_ld32(t_s + (uint32_t)(half * 32), x);
+            // (written before the tile's conversion was handed over, and so before its S; the slot is written again after
+            // the P.V of tile k + 1)
+            const int k_ref = ms.ref[k & 3][0], v_ref = ms.ref[k & 3][1];
+            float sc = sc_row * exp2_int(k_ref);
+            if (sc < 0x1p-126f) sc = 0x1p-126f;  // (a zero would turn masked scores into NaN)
             tmem_wait_ld();
             const int j0 = n * BN + half * 32;
             if (j0 + 31 > first + row0 + t * BM) {  // causal mask, on columns that reach past the tile's first row
