@@ -14,10 +14,14 @@
 // free list, not from the table entry.
 // Up to kManyThreads requests a thread has one request (ONE), and what the tokens need of it (its length, its pages, the
 // page that it fills first, and the head of the free list) is fetched beside the sums and kept in shared memory: the map of a
-// decode step then has two dependent global loads in a row instead of five.  64 requests with a token each 4.4 us against
-// 4.8 without, 512 requests 5.6 against 6.1; 1024 prompts of up to 1023 tokens 7.35 against 7.25.
+// decode step then has two dependent global loads in a row instead of five: 512 requests with a token each 5.6 us against
+// 6.1 without, 256 requests of up to 127 tokens 4.8 against 5.3 (both with four tokens a thread).
 // CTAs of kFewThreads threads up to as many requests, of kManyThreads beyond: 256 requests of up to 127 tokens 4.8 us against
-// 6.1 with the larger CTAs, 64 requests 4.4 against 4.8.
+// 6.1 with the larger CTAs.
+// A thread maps one token while the buffer is small enough (each token is a search of its own then, side by side): 64
+// requests with a token each 3.0 us against 4.0 with four a thread, 256 requests of up to 127 tokens 3.4 against 4.5,
+// a buffer of 160000 rows 4.5 against 4.7.  Beyond, four, which share a search and a 16-byte store: 270000 rows 4.75 us
+// against 5.05, 2^20 rows of 1024 requests 7.2 against 8.8.
 #include "common.cuh"
 #include "internal.h"
 
@@ -26,7 +30,7 @@ namespace diffqkv {
 namespace {
 
 constexpr int kFewThreads = 256, kManyThreads = 1024;
-constexpr int kMapTokens = 4;  // consecutive tokens a thread maps (one 16-byte store per output)
+constexpr int kMapTokens = 4;  // consecutive tokens a thread maps in large buffers (one 16-byte store per output)
 
 struct PageMapArgs {
     const int32_t *seq_lens, *new_lens, *free_pages;
@@ -81,7 +85,8 @@ __device__ __forceinline__ int checked_page(const PageMapArgs &a, int page) {
 }
 
 // ONE: at most THREADS requests, one a thread.
-template <int THREADS, bool ONE>
+// TOKENS: consecutive tokens of a thread.
+template <int THREADS, bool ONE, int TOKENS>
 __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ int tok_s[THREADS], pag_s[THREADS];  // tokens and pages before each run
@@ -183,12 +188,12 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
         a.block_table[(size_t)b * a.max_blocks + have + (k - off)] = checked_page(a, free_page(k));
     }
 
-    // slots and positions, kMapTokens consecutive tokens a thread
-    for (long long i0 = (long long)(blockIdx.x * THREADS + tid) * kMapTokens; i0 < a.capacity;
-         i0 += (long long)stride * kMapTokens) {
-        int slot[kMapTokens], pos[kMapTokens];
+    // slots and positions, TOKENS consecutive tokens a thread
+    for (long long i0 = (long long)(blockIdx.x * THREADS + tid) * TOKENS; i0 < a.capacity;
+         i0 += (long long)stride * TOKENS) {
+        int slot[TOKENS], pos[TOKENS];
 #pragma unroll
-        for (int e = 0; e < kMapTokens; ++e) slot[e] = pos[e] = -1;
+        for (int e = 0; e < TOKENS; ++e) slot[e] = pos[e] = -1;
         if (i0 < tokens) {
             int run = last_not_above(tok_s, runs, (int)i0);
             int b = run * a.per, at = tok_s[run], off = pag_s[run], s, have, end;
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
             }
             int seen = -1, page = -1;  // logical page last looked up, and its pool page
 #pragma unroll
-            for (int e = 0; e < kMapTokens; ++e) {
+            for (int e = 0; e < TOKENS; ++e) {
                 const int i = (int)i0 + e;
                 if (i >= tokens) break;
                 while (i >= end) {
@@ -238,11 +243,11 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
                 if (page >= 0) slot[e] = page * a.page_size + (pos[e] - lp * a.page_size);
             }
         }
-        if (i0 + kMapTokens <= a.capacity) {
-            *reinterpret_cast<int4 *>(a.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-            if (a.positions) *reinterpret_cast<int4 *>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (TOKENS == 4 && i0 + TOKENS <= a.capacity) {
+            *reinterpret_cast<int4 *>(a.slot_map + i0) = make_int4(slot[0], slot[1 % TOKENS], slot[2 % TOKENS], slot[3 % TOKENS]);
+            if (a.positions) *reinterpret_cast<int4 *>(a.positions + i0) = make_int4(pos[0], pos[1 % TOKENS], pos[2 % TOKENS], pos[3 % TOKENS]);
         } else {
-            for (int e = 0; i0 + e < a.capacity; ++e) {
+            for (int e = 0; e < TOKENS && i0 + e < a.capacity; ++e) {
                 a.slot_map[i0 + e] = slot[e];
                 if (a.positions) a.positions[i0 + e] = pos[e];
             }
@@ -292,16 +297,19 @@ diffqkv_status_t page_map_launch(int32_t batch, const int32_t *seq_lens, const i
         for (a.page_shift = 0; (1 << a.page_shift) < page_size;) ++a.page_shift;
     const int threads = batch <= kFewThreads ? kFewThreads : kManyThreads;
     a.per = (batch + threads - 1) / threads;
-    // enough CTAs for one sweep over the tokens, at most as many as the SMs hold
-    const long long want = ((long long)capacity + threads * kMapTokens - 1) / (threads * kMapTokens);
+    // CTAs as many as the SMs hold, fewer where one sweep over the tokens takes fewer; a token a thread up to one and a
+    // half such sweeps
     const long long most = (long long)dev.num_sms * (threads == kFewThreads ? 4 : 1);
+    const int tok = 2LL * capacity <= 3LL * most * threads ? 1 : kMapTokens;
+    const long long want = ((long long)capacity + threads * tok - 1) / (threads * tok);
     const int grid = (int)(want < 1 ? 1 : want > most ? most : want);
+    auto launch = [&](auto one, auto four) { (tok == 1 ? one : four)<<<grid, threads, 0, stream>>>(a); };
     if (batch <= kFewThreads)
-        page_map_kernel<kFewThreads, true><<<grid, kFewThreads, 0, stream>>>(a);
+        launch(page_map_kernel<kFewThreads, true, 1>, page_map_kernel<kFewThreads, true, kMapTokens>);
     else if (batch <= kManyThreads)
-        page_map_kernel<kManyThreads, true><<<grid, kManyThreads, 0, stream>>>(a);
+        launch(page_map_kernel<kManyThreads, true, 1>, page_map_kernel<kManyThreads, true, kMapTokens>);
     else
-        page_map_kernel<kManyThreads, false><<<grid, kManyThreads, 0, stream>>>(a);
+        launch(page_map_kernel<kManyThreads, false, 1>, page_map_kernel<kManyThreads, false, kMapTokens>);
     return cudaGetLastError() == cudaSuccess ? DIFFQKV_OK : DIFFQKV_ERR_CUDA;
 }
 

@@ -52,6 +52,14 @@ def test_against_the_definition(cuda_device, batch, hi, new_hi, page):
         _check(s, n, table, free, page, num_pages, sum(n) + extra, cuda_device)
 
 
+@pytest.mark.parametrize("batch,hi,new_hi,page", [(7, 100, 60000, 16), (300, 90, 1500, 24), (1500, 300, 300, 32)])
+def test_large_buffers(cuda_device, batch, hi, new_hi, page):
+    """Buffers beyond the size up to which a thread maps one token: four, with ends of every remainder."""
+    s, n, table, free, num_pages = _step(batch, hi, new_hi, page, batch)
+    for capacity in (sum(n) + 230000, sum(n) + 230001, sum(n) + 230003):
+        _check(s, n, table, free, page, num_pages, capacity, cuda_device)
+
+
 def test_many_requests_with_long_stretches_of_empty_ones(cuda_device):
     batch, page = 5000, 16
     n = [0] * batch
