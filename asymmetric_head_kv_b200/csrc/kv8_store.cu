@@ -19,16 +19,18 @@
 // maximum and the rounding (longer runs are read twice).  The first rows are requested together with the slots,
 // before it is known which run they belong to: most often they are the ones.
 // Shapes of group, by the rows a run can have (4 heads of 64 and 16 of 128 unless stated, inputs beyond L2):
-//  * `share` warps over the runs that begin in the CTA's chunk of tokens: one warp (CTAs of four) where it holds a block in
-//    registers (16 rows of 128 or 32 of 64), otherwise as many as do (CTAs of eight); the maximum crosses a warp in one
-//    redux and the warps through shared memory.  16384 tokens in blocks of 16: 25.5 us, 4.4 TB/s, 0.69 of the copy rate;
-//    CTAs of eight for one warp: 27.7.  Blocks of 64, 3704 tokens of 16 + 16 heads of 128: 17.3 us shared, 21.0 with one
-//    warp; 128: 50 against 54 (16384 tokens); blocks of 64 with 16384 tokens would be 36 against 38 the other way.
-//    What keeps it from the copy rate: the CTAs' start (slots, run, rows: two loads deep) is not hidden by others' work.
+//  * `share` warps over the runs that begin in the CTA's chunk of tokens.  One warp (CTAs of four) where it holds a block in
+//    registers (16 rows of 128 or 32 of 64) and where the call has kWarpsPerSm (run, head)s an SM or more; otherwise two,
+//    four or eight (CTAs of eight) up to one of the two; the maximum crosses a warp in one redux and the warps through
+//    shared memory.  16384 tokens in blocks of 16: 25.5 us, 4.4 TB/s, 0.69 of the copy rate (27.7 with CTAs of
+//    eight for one warp); of 64: 30 us (35.6 with four warps each), of 128: 37 (47 with eight).  1024 tokens in blocks of
+//    128: 6.9 us shared, 15.2 with one warp; 4096: 13.8 against 21.6.
+//    Slots come 64 tokens at a time, side by side, so that a run of up to 32 tokens is known without another load.  What keeps
+//    it from the copy rate: issue slots (66% used) and the CTAs' start, two loads deep.
 //  * a chunk of one token for up to kFewTokens, so that a decode step's heads and requests spread over the SMs: 16 tokens
-//    3.5 us against 4.9 with chunks of 16, 256 tokens 4.5 against 5.4, but 512 tokens 5.9 against 5.2.
+//    3.5 us against 4.6 with chunks of 16, 256 tokens 4.5 against 5.0, but 512 tokens 6.0 against 5.0.
 //  * blocks of up to kRowBlock positions in larger steps: the 8 or 16 lanes of one row take kRowVec tokens and the runs
-//    that begin there.  16384 tokens: blocks of one 68 us (a warp a run: 186), of four 36 us (a warp: 58).
+//    that begin there.  16384 tokens: blocks of one 68 us (a warp a run: 174), of four 36 us (a warp: 53).
 #include <algorithm>
 #include <type_traits>
 
@@ -43,6 +45,7 @@ constexpr int kStoreWarps = 8;
 constexpr int kRunVec = 8, kRowVec = 4;  // 16-byte loads a lane keeps, by shape of group
 constexpr int kMaxTokens = 32; // tokens whose runs one CTA may lead
 constexpr int kRowBlock = 4;   // blocks up to this size take a row's lanes
+constexpr int kWarpsPerSm = 16;  // (run, head)s an SM from which a warp each is enough
 constexpr int kFewTokens = 256;
 constexpr int run_warps(bool shared) { return shared ? kStoreWarps : kStoreWarps / 2; }
 
@@ -211,38 +214,37 @@ __global__ void __launch_bounds__(run_warps(SHARED) * 32, 24 / run_warps(SHARED)
             if (i < a.chunk && t_begin + i < a.tokens) keep[v] = __ldg(x + (size_t)(t_begin + i) * n * lpr);
         }
     }
-    // every warp finds the runs its CTA leads: lane i looks at token t_begin + i
-    const int t = t_begin + lane;
-    int slot = -1, blk = -1;
-    bool leads = false;
-    if (lane < a.chunk && t < a.tokens) {
-        const int raw = __ldg(a.slot_map + t);
-        const int before = t > 0 ? slot_of(a, t - 1) : -1;
-        if (raw >= a.slots && warp == 0 && blockIdx.y == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
-        slot = raw < a.slots ? raw : -1;
-        if (slot >= 0) {
-            blk = block_of(a, slot);
-            leads = before < 0 || block_of(a, before) != blk;
-        }
-    }
+    // every warp finds the runs its CTA leads: lane i has the slots of tokens t_begin + i and t_begin + 32 + i
+    const int t = t_begin + lane, raw = t < a.tokens ? __ldg(a.slot_map + t) : -1;
+    const int far = t + 32 < a.tokens ? slot_of(a, t + 32) : -1;
+    const int ahead = lane == 0 && t > 0 ? slot_of(a, t - 1) : -1;
+    if (raw >= a.slots && lane < a.chunk && warp == 0 && blockIdx.y == 0) record_error(a.status, DIFFQKV_ERR_DEVICE_PAGE);
+    const int slot = raw < a.slots ? raw : -1, blk = slot >= 0 ? block_of(a, slot) : -1;
+    int before = __shfl_up_sync(0xffffffffu, blk, 1);
+    if (lane == 0) before = ahead >= 0 ? block_of(a, ahead) : -1;
+    const bool leads = lane < a.chunk && blk >= 0 && before != blk;
     if (head >= heads) return;
     for (unsigned left = __ballot_sync(0xffffffffu, leads); left; left &= left - 1) {
         const int src = __ffs(left) - 1;
         const int t0 = t_begin + src;
         const int run_blk = __shfl_sync(0xffffffffu, blk, src);
-        // the run's length and lowest row, 32 tokens at a time
+        // the run's length and lowest row, 32 tokens at a time; a block's rows are all that a run can have
         int len = 0, low = a.sb;
         for (bool open = true; open; len += 32) {
             const int tt = t0 + len + lane;
-            const int s = tt < a.tokens ? slot_of(a, tt) : -1;
-            const bool in = s >= 0 && block_of(a, s) == run_blk;
-            const unsigned out = __ballot_sync(0xffffffffu, !in);
-            const int n = out ? __ffs(out) - 1 : 32;
-            low = min(low, (int)__reduce_min_sync(0xffffffffu, lane < n ? (unsigned)(s - run_blk * a.sb) : 0x7fffffffu));
-            if (n < 32) {
-                len += n - 32;
-                open = false;
+            int s;
+            if (len == 0) {
+                const int x = __shfl_sync(0xffffffffu, slot, src + lane & 31), y = __shfl_sync(0xffffffffu, far, src + lane & 31);
+                s = src + lane < 32 ? x : y;
+            } else {
+                s = tt < a.tokens ? slot_of(a, tt) : -1;
             }
+            const unsigned row = (unsigned)(s - run_blk * a.sb);
+            const unsigned out = __ballot_sync(0xffffffffu, s < 0 || row >= (unsigned)a.sb);
+            const int n = out ? __ffs(out) - 1 : 32;
+            low = min(low, (int)__reduce_min_sync(0xffffffffu, lane < n ? row : 0x7fffffffu));
+            open = n == 32 && len + 32 < a.sb;
+            if (n < 32) len += n - 32;
         }
         const bool kept = !SHARED && src == 0 && len <= a.chunk;
         if (head < a.n_k)
@@ -365,7 +367,9 @@ diffqkv_status_t kv8_store_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cac
     a.chunk = tokens <= kFewTokens ? 1 : std::min(kMaxTokens, std::max(16, a.sb));
     a.share = 1;
     if (tokens > kFewTokens)
-        while (a.share < kStoreWarps && a.share * 32 * kRunVec * 8 / std::max(d->d_k, d->d_v) < a.sb) a.share *= 2;
+        while (a.share < kStoreWarps && a.share * 32 * kRunVec * 8 / std::max(d->d_k, d->d_v) < a.sb &&
+               (long long)tokens * (d->n_k + d->n_v) / a.sb * a.share < kWarpsPerSm * dev.num_sms)
+            a.share *= 2;
     if ((d->n_k + d->n_v) > 65535) return DIFFQKV_ERR_UNSUPPORTED;
     if ((long long)tokens * std::max(d->n_k, d->n_v) * 16 > 0x7fffffffLL) return DIFFQKV_ERR_UNSUPPORTED;  // thread index
     if (d->d_k == 64)

@@ -86,6 +86,27 @@ def test_a_block_longer_than_the_registers(cuda_device):
     p.store(*p.rows(700, 1), list(range(100, 800)))
 
 
+@pytest.mark.parametrize("shape", ["diffqkv", "k_wide"])
+@pytest.mark.parametrize("T,page,sb", [(300, 128, 128), (700, 256, 256), (2000, 64, 64), (5000, 32, 32), (6000, 128, 64),
+                                       (9000, 64, 64), (3000, 24, 12)])
+def test_long_blocks_shared_and_whole(cuda_device, shape, T, page, sb):
+    """Runs that begin and end anywhere, by one warp (long and short of its registers), two, four and eight."""
+    pages = T // page + 12
+    p = Pools(pages, page, sb, SHAPES[shape], cuda_device, seed=T)
+    ids = torch.randperm(pages, generator=torch.Generator().manual_seed(T)).tolist()
+    slots, at, n = [], 0, 1
+    while len(slots) < T:  # requests on pages of their own, each from a row of its own, a skipped token between them
+        n = min(n * 3 % 997 + 1, T - len(slots))
+        start = (5 * n) % page if len(ids) - at > -(-(n + page) // page) else 0
+        need = -(-(start + n) // page)
+        if at + need > len(ids):
+            break
+        slots += _slots(page, ids[at:at + need], start, n) + [-1]
+        at += need
+    slots += [-1] * (T - len(slots))
+    p.store(*p.rows(len(slots), 3), slots)
+
+
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan"), 3.3e38, 2.0 ** -133, 0.0])
 def test_special_values(cuda_device, value):
     p = Pools(4, 16, 16, SHAPES["diffqkv"], cuda_device)
