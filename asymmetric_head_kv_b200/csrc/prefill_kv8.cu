@@ -21,13 +21,13 @@
 //  * Rows of Q come in, and rows of the output go out, with a row's 16-byte pieces in neighbouring lanes.
 //  * Units are taken longest first.  Where they are fewer than half of the SMs, each is cut into pieces of equal length, one
 //    CTA each; records in the workspace, merged by the last CTA of the unit: 256 rows over 131072 positions, 16 heads, in
-//    270 us with 9 pieces a unit, 527 with 4.
+//    266 us with 9 pieces a unit, 527 with 4.
 //    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
 //    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
 // What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
-// their latencies.  Two prompts of 8192, 16 heads of 64/128: 495 us, 832 TFLOP/s, 0.49 of the measured GEMM peak (tensor
-// pipe 35% busy, XU 47%, 53% of issue slots); 4 rows-of-17 requests of 1003 positions: 20.7 us, of which about 14 are one
-// CTA's start and end.
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 485 us, 850 TFLOP/s, 0.50 of the measured GEMM peak (tensor
+// pipe 39% busy, XU 53%, 59% of issue slots); four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
+// one CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>
 
