@@ -64,7 +64,8 @@ def _decode_dims(q, k_cache, v_cache, scale):
 
 
 def decode_workspace(q_or_dims, k_cache=None, v_cache=None, device=None) -> torch.Tensor:
-    """Zero-filled workspace for :func:`decode` (reusable across calls of one shape)."""
+    """Zero-filled workspace for :func:`decode`, its variants and :func:`decode_paged_kv8` (reusable, without clearing, by
+    calls of any shape that it is large enough for)."""
     dims = q_or_dims if isinstance(q_or_dims, Dims) else _decode_dims(q_or_dims, k_cache, v_cache, 1.0)[0]
     n = lib().diffqkv_decode_workspace_size(ctypes.byref(dims))
     if n == 0:
@@ -262,7 +263,8 @@ def decode_from_host(q_host, k_host, v_host, seq_lens_host, out_host, dev_buffer
 
 
 def decode_topv_workspace(dims: Dims, t_max: int, topk: int, device="cuda") -> torch.Tensor:
-    """Workspace for :func:`decode_topv`; zero-filled (its 256-byte header holds the error word)."""
+    """Workspace for :func:`decode_topv`; zero-filled (its 256-byte header holds the error word).  Reusable without clearing
+    by calls of the same batch and head counts."""
     n = lib().diffqkv_decode_topv_workspace_size(ctypes.byref(dims), t_max, topk)
     if n == 0:
         raise DiffqkvError(_capi.INVALID_ARG, "decode_topv_workspace_size")
@@ -489,7 +491,8 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
 
 
 def prefill_paged_kv8_workspace(dims: Dims, device="cuda") -> torch.Tensor:
-    """Zero-filled workspace for :func:`prefill_paged_kv8` (reusable across calls, whatever their sizes)."""
+    """Zero-filled workspace for :func:`prefill_paged_kv8` (reusable across calls, whatever their sizes; one that is large
+    enough may serve the decode calls too)."""
     n = lib().diffqkv_prefill_paged_kv8_workspace_size(dims)
     if n == 0:
         raise DiffqkvError(_capi.INVALID_ARG, "prefill_paged_kv8_workspace_size")

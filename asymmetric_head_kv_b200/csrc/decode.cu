@@ -51,8 +51,7 @@ namespace diffqkv {
 
 namespace {
 
-constexpr int kGridMax = 2048;        // upper bound of split-kernel CTAs (sizes the workspace)
-constexpr int kWorkspaceHeader = 256; // reserved
+constexpr int kGridMax = kWsCounters; // upper bound of split-kernel CTAs (sizes the workspace; one counter each)
 constexpr int kPartialPad = 4;        // per-head partial record: o[d_v], m, l, pad, pad
 
 struct DecodeArgs {
@@ -443,9 +442,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1)
                 }
             }
             named_barrier(1, NCW * 32);
-            const long long u = (long long)w.b * a.n_k + w.g;
+            const long long u = (long long)w.b * a.n_k + w.g, units = (long long)a.batch * a.n_k;
             const long long first = cta_of_tile(w.P, N, Ge);
             const long long last = cta_of_tile(w.P + w.nt - 1, N, Ge);
+            const long long counter = counter_of(u, first, units, kWsCounters);
             if (r == 0) {
                 float M = m_run, L = l_run;
                 float O[8];
@@ -481,8 +481,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1)
             __threadfence();
             named_barrier(1, NCW * 32);
             if (tid == 0) {
-                const unsigned old =
-                    in_bounds(u, (long long)a.batch * a.n_k, a.status) ? atomicAdd(a.counters + u, 1u) : 0u;
+                // (a unit that this CTA has all of needs no count)
+                unsigned old = 0;
+                if (first != last && in_bounds(counter, min(units, (long long)kWsCounters), a.status))
+                    old = atomicAdd(a.counters + counter, 1u);
                 *last_flag = (old == (unsigned)(last - first)) ? 1 : 0;
             }
             named_barrier(1, NCW * 32);
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1)
                     if (in_bounds((long long)w.b * a.n_q + w.g * QPK + h2, (long long)a.batch * a.n_q, a.status))
                         *reinterpret_cast<uint2 *>(a.out + ((size_t)w.b * a.n_q + w.g * QPK + h2) * DV + d4 * 4) = packed;
                 }
-                if (tid == 0) a.counters[u] = 0u;
+                if (tid == 0 && first != last) a.counters[counter] = 0u;
             }
             named_barrier(1, NCW * 32);
         }
@@ -679,9 +681,7 @@ size_t decode_workspace_size(const diffqkv_dims_t *d) {
     if (validate_dims(d) != DIFFQKV_OK) return 0;
     const size_t units = (size_t)d->batch * d->n_k;
     const size_t qpk = d->n_q / d->n_k;
-    const size_t counters = align_up(units * sizeof(uint32_t), 256);
-    const size_t partials = (units + kGridMax) * qpk * (d->d_v + kPartialPad) * sizeof(float);
-    return kWorkspaceHeader + counters + partials;
+    return kWsRecords + (units + kGridMax) * qpk * (d->d_v + kPartialPad) * sizeof(float);
 }
 
 diffqkv_status_t decode_plan(const diffqkv_dims_t *d, int32_t t_max, int32_t max_seq_len, int32_t num_sms,
@@ -812,8 +812,8 @@ diffqkv_status_t decode_prepare(const diffqkv_dims_t *d, const void *q, const vo
     }
     a.seq_lens = seq_lens;
     a.out = static_cast<__nv_bfloat16 *>(out);
-    a.counters = reinterpret_cast<uint32_t *>(ws + kWorkspaceHeader);
-    a.partials = reinterpret_cast<float *>(ws + kWorkspaceHeader + align_up(units * sizeof(uint32_t), 256));
+    a.counters = reinterpret_cast<uint32_t *>(ws + kWsHeader);
+    a.partials = reinterpret_cast<float *>(ws + kWsRecords);
     a.status = reinterpret_cast<int32_t *>(ws);  // the workspace's own error word
     a.partial_slots = (long long)units + kGridMax;
     a.store_rows = paged ? (long long)paged->num_pages * paged->page_size : (long long)d->batch * t_max;
@@ -942,10 +942,10 @@ diffqkv_status_t decode_noalloc_launch(const diffqkv_dims_t *d, const void *q, c
     KernelFn fn = pick_kernel(d->d_k, d->d_v, qpk);
     if (!fn) return DIFFQKV_ERR_UNSUPPORTED;
 
-    // scratch: header, one counter per unit, then partial slots u + c < units + grid
+    // scratch: header, one counter per unit (the first kWsCounters of them in use), then partial slots u + c < units + grid
     const size_t units = (size_t)d->batch * d->n_k;
     const size_t counter_bytes = align_up(units * sizeof(uint32_t), 256);
-    const size_t need = kWorkspaceHeader + counter_bytes +
+    const size_t need = kWsHeader + counter_bytes +
                         (units + (size_t)plan.grid_ctas) * qpk * (d->d_v + kPartialPad) * sizeof(float);
     if (need > (size_t)DIFFQKV_NOALLOC_SCRATCH_BYTES) return DIFFQKV_ERR_SCRATCH_LIMIT;
     uint8_t *scratch = nullptr;
@@ -964,10 +964,10 @@ diffqkv_status_t decode_noalloc_launch(const diffqkv_dims_t *d, const void *q, c
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.seq_lens = seq_lens;
     a.out = static_cast<__nv_bfloat16 *>(out);
-    a.counters = reinterpret_cast<uint32_t *>(scratch + kWorkspaceHeader);
+    a.counters = reinterpret_cast<uint32_t *>(scratch + kWsHeader);
     a.partial_slots = (long long)units + plan.grid_ctas;
     a.store_rows = (long long)d->batch * t_max;
-    a.partials = reinterpret_cast<float *>(scratch + kWorkspaceHeader + counter_bytes);
+    a.partials = reinterpret_cast<float *>(scratch + kWsHeader + counter_bytes);
     a.status = dev.status_word;
     a.batch = d->batch;
     a.n_q = d->n_q;

@@ -55,8 +55,7 @@ constexpr int kMmaWarp = 4, kKWarp = 5, kVWarp = 6, kScaleWarp0 = 7, kScaleWarps
 constexpr int kThreads = 32 * (kScaleWarp0 + kScaleWarps);
 constexpr int kMaxVSlots = 12;
 constexpr int k_stages(int dk) { return dk == 64 ? 3 : 2; }
-constexpr int kGridMax = 2048;         // as in decode.cu: sizes the workspace
-constexpr int kHeader = 256;
+constexpr int kGridMax = kWsCounters;  // as in decode.cu: sizes the workspace
 constexpr int kPad = 4;                // a partial record: o[d_v], m, l, pad, pad
 constexpr float kTop = 8.f;            // weights at the reference are 2^kTop, the largest that split3 takes
 constexpr float kMaxSlack = 64.f;      // growth of the row sum's own maximum
@@ -630,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const long long u = (long long)w.b * a.n_k + w.g;
                 const long long first = cta_of_tile(w.P, N, Ge), last = cta_of_tile(w.P + w.nt - 1, N, Ge);
                 const bool whole = first == last;  // no other CTA has a piece: straight to the output
+                const long long counter = counter_of(u, first, (long long)a.batch * a.n_k, kWsCounters);
                 const bool slot_ok = in_bounds(u + c, a.partial_slots, a.status);
 #pragma unroll 1
                 for (int h = 0; h < QPK; ++h) {
@@ -664,8 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __threadfence();
                 named_barrier(1, kSoftmaxThreads);
                 if (tid == 0) {
-                    const unsigned old =
-                        in_bounds(u, (long long)a.batch * a.n_k, a.status) ? atomicAdd(a.counters + u, 1u) : 0u;
+                    const unsigned old = in_bounds(counter, kWsCounters, a.status) ? atomicAdd(a.counters + counter, 1u) : 0u;
                     ms.last_flag = old == (unsigned)(last - first) ? 1 : 0;
                 }
                 named_barrier(1, kSoftmaxThreads);
@@ -717,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             *reinterpret_cast<uint2 *>(a.out + row * DV + d4 * 4) =
                                 make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
                     }
-                    if (tid == 0) a.counters[u] = 0u;
+                    if (tid == 0) a.counters[counter] = 0u;
                 }
                 named_barrier(1, kSoftmaxThreads);
             }
@@ -845,8 +844,8 @@ diffqkv_status_t decode_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_ca
     a.block_table = block_table;
     a.seq_lens = seq_lens;
     a.out = static_cast<__nv_bfloat16 *>(out);
-    a.counters = reinterpret_cast<uint32_t *>(ws + kHeader);
-    a.partials = reinterpret_cast<float *>(ws + kHeader + (units * sizeof(uint32_t) + 255) / 256 * 256);
+    a.counters = reinterpret_cast<uint32_t *>(ws + kWsHeader);
+    a.partials = reinterpret_cast<float *>(ws + kWsRecords);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.batch = d->batch;
     a.n_q = d->n_q;

@@ -38,6 +38,13 @@ __device__ __forceinline__ long long cta_of_tile(long long t, long long N, long 
     return ((t + 1) * G - 1) / N;
 }
 
+// Counter (of `counters`) in which the CTAs of a unit that more than one of them has a piece of count these pieces: the
+// unit's own where there are as many counters as units, else that of the unit's first CTA.  A CTA is that for one such
+// unit at most, the one its range ends inside of.
+__device__ __forceinline__ long long counter_of(long long u, long long first, long long units, int counters) {
+    return units <= counters ? u : first;
+}
+
 // Run by one warp: total tile count N and the unit holding the first tile of CTA c of G, into
 // scan_s = {N, P0, b0 << 32 | g0, i0}.  CTA 0 flags lengths outside [0, t_max] (status).
 template <int TT, class Args>

@@ -58,6 +58,13 @@ diffqkv_status_t validate_dims(const diffqkv_dims_t *d);
 // kv8_store.cu: checks of an 8-bit cache (dims, pools, page and block sizes).
 diffqkv_status_t validate_kv8(const diffqkv_dims_t *d, const diffqkv_kv8_cache_t *c);
 
+// Workspace of the calls that split a unit over CTAs (decode, 8-bit decode, 8-bit prefill): a header whose first word is the
+// error word, kWsCounters counters that are zero between calls, then the records of the pieces.  Nothing of it moves with
+// a call's sizes, so a call's records never lie where another one, of any shape or operator, counts.
+constexpr size_t kWsHeader = 256;
+constexpr int kWsCounters = 2048;
+constexpr size_t kWsRecords = kWsHeader + kWsCounters * sizeof(uint32_t);
+
 // decode.cu
 // A paged K/V cache: pools [num_pages, page_size, heads, d] for K and for V and
 // one block table [batch, max_blocks] (device int32) of pool pages.

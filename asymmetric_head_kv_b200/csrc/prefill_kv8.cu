@@ -50,7 +50,6 @@ constexpr int kRaw = 4;         // stages of codes
 constexpr int kScaleSlots = 8;  // tiles of scales, fetched four at a time
 constexpr int kSlots = 160;     // partial records of the workspace: one for each piece of a call whose units are cut
 constexpr int kCutBatch = 32;   // requests, at most, of a call whose units are cut
-constexpr int kHeader = 256;
 constexpr float kRescale = 8.f;  // growth (log2) of a row's maximum before O is rescaled
 constexpr float kShift = 7.f;    // weights are held at 2^kShift of the reference
 
@@ -843,7 +842,8 @@ PreFn plan(int *smem) {
 
 size_t prefill_kv8_workspace_size(const diffqkv_dims_t *d) {
     if (validate_dims(d) != DIFFQKV_OK) return 0;
-    return kHeader + kSlots * sizeof(uint32_t) + 256 + (size_t)kSlots * kRows * (d->d_v + 2) * sizeof(float);
+    static_assert(kSlots <= kWsCounters, "a counter for each record");
+    return kWsRecords + (size_t)kSlots * kRows * (d->d_v + 2) * sizeof(float);
 }
 
 diffqkv_status_t prefill_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cache_t *cache, const void *q,
@@ -900,8 +900,8 @@ diffqkv_status_t prefill_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_c
     a.seq_lens = seq_lens;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.status = reinterpret_cast<int32_t *>(ws);
-    a.counters = reinterpret_cast<uint32_t *>(ws + kHeader);
-    a.partials = reinterpret_cast<float *>(ws + (kHeader + kSlots * sizeof(uint32_t) + 255) / 256 * 256);
+    a.counters = reinterpret_cast<uint32_t *>(ws + kWsHeader);
+    a.partials = reinterpret_cast<float *>(ws + kWsRecords);
     a.batch = d->batch;
     a.n_q = d->n_q;
     a.n_k = d->n_k;

@@ -96,12 +96,16 @@ int32_t diffqkv_version(void);
 /* Bytes of workspace diffqkv_decode needs for this shape (0 if dims are
  * invalid).  Depends only on the dims, not on the device or the lengths.
  * The workspace must be zero-filled before its FIRST use (cudaMemset, or
- * diffqkv_workspace_init); every call that completes leaves it zero-filled
- * again (its error word aside, which keeps the first device-side error until
- * diffqkv_workspace_status reads it), so it can be reused without clearing.
- * Two calls that may run concurrently must not share a workspace.  Layout: a
- * 256-byte header whose first 32-bit word is the error word, then one counter
- * per (batch, K head), then the split partials. */
+ * diffqkv_workspace_init).  Layout, the same for every shape: a 256-byte header
+ * whose first 32-bit word is the error word, 2048 32-bit counters, then the
+ * split partials.  Every call that completes leaves header and counters zero
+ * again (the error word aside, which keeps the first device-side error until
+ * diffqkv_workspace_status reads it) and reads no partial that it has not
+ * written, so one workspace, large enough for the largest of them, serves
+ * calls of any dims one after another without clearing: diffqkv_decode, its
+ * variants, diffqkv_decode_paged_kv8 and diffqkv_prefill_paged_kv8 alike.
+ * (After a call that reported DIFFQKV_ERR_DEVICE_TIMEOUT, zero-fill it again.)
+ * Two calls that may run concurrently must not share a workspace. */
 size_t diffqkv_decode_workspace_size(const diffqkv_dims_t *dims);
 
 /* Zero-fill a workspace on `stream` (cudaMemsetAsync). */
@@ -306,9 +310,11 @@ diffqkv_status_t diffqkv_decode_from_host(const diffqkv_dims_t *dims, const void
 
 /* Workspace bytes for diffqkv_decode_topv (0 if invalid).  Zero-fill it
  * before its first use (diffqkv_workspace_init); every call that completes
- * leaves it reusable without clearing (its error word aside, which keeps the
- * first device-side error until diffqkv_workspace_status reads it).  After a
- * call that reported DIFFQKV_ERR_DEVICE_TIMEOUT, zero-fill it again.  Layout,
+ * leaves it reusable without clearing by calls of the same batch, n_q and n_k
+ * (its error word aside, which keeps the first device-side error until
+ * diffqkv_workspace_status reads it).  Where the counters end moves with
+ * these: zero-fill it before a call of others, or of another operator, and
+ * after a call that reported DIFFQKV_ERR_DEVICE_TIMEOUT.  Layout,
  * with R = batch * n_q rows and U = batch * n_k (batch, K head) units, each
  * region starting on a 256-byte boundary:
  *   - a 256-byte header whose first 32-bit word is the error word;
@@ -577,7 +583,8 @@ diffqkv_status_t diffqkv_decode_paged_kv8(const diffqkv_dims_t *dims, const diff
                                           size_t workspace_bytes, diffqkv_stream_t stream);
 
 /* Bytes of workspace diffqkv_prefill_paged_kv8 needs (0 if dims are invalid); zero-filled
- * before its first use, and left reusable by every call that completes, as diffqkv_decode's. */
+ * before its first use, and left reusable by every call that completes, as diffqkv_decode's (whose layout it has; the size
+ * does not depend on the batch). */
 size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
 
 /*
