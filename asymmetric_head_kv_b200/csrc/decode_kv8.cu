@@ -20,9 +20,13 @@
 //    maxima cross the 128 threads by one redux a head and one shared-memory exchange.
 //  * O^T = V^T P^T: M = d_v, N = 16 columns of P (the terms of up to five heads), K = 128 positions: V tiles are
 //    used as they lie in the cache, positions in rows (an MN-major A operand).
-//  * R is the reference of the output's exponent, score and V scale together: the running maximum of (a tile's largest
-//    score + its largest V exponent), so that weights are at most 2^8.  O is rescaled in TMEM when it grows, a few times
-//    a unit.  (A slack that saves rescales would take as many bits from the small weights.)
+//  * R is the reference of the output's exponent, score and V scale together: the running maximum of a position's score + its
+//    block's V exponent, so that weights are at most 2^8 and the largest is that.  (The largest score plus the largest
+//    exponent of a tile would bound the weights too, but a block of large scale and little weight would then lift R
+//    above every weight and take its bits.)  O is rescaled in TMEM when it grows, a few times a unit.  (A slack that saves
+//    rescales would take as many bits from the small weights.)  The row sum needs a reference too, of the score alone; it
+//    may lie some way below the largest one, fp32 has the range: R's candidate less the tile's largest V exponent, where
+//    the tile's exponents are close together, so that one maximum a head serves both.
 //  * work split, ragged batches, ring of TMA stages, partials and the combine by the last CTA of a unit are those of
 //    decode.cu.  K tiles and V head tiles have rings of their own (a V slot is one head of one tile: any number of V
 //    heads per K head fits), the K tile of the next step is requested before the V tiles of this one.
@@ -58,7 +62,9 @@ constexpr int k_stages(int dk) { return dk == 64 ? 3 : 2; }
 constexpr int kGridMax = kWsCounters;  // as in decode.cu: sizes the workspace
 constexpr int kPad = 4;                // a partial record: o[d_v], m, l, pad, pad
 constexpr float kTop = 8.f;            // weights at the reference are 2^kTop, the largest that split3 takes
-constexpr float kMaxSlack = 64.f;      // growth of the row sum's own maximum
+constexpr float kMaxSlack = 48.f;      // growth of the row sum's own reference
+constexpr int kSpread = 32;            // of a tile's V exponents, for which that reference is taken from R's; together with the
+                                       // slack a term of the row sum is at most 2^80, the sum of 2^31 of them below 2^112
 
 struct Kv8Args {
     const __nv_bfloat16 *q;
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int j = warp - kScaleWarp0;
         int8_t *ke = reinterpret_cast<int8_t *>(sc_s + j * a.sc_bytes);  // [128] K exponents, then [vpg][128] of V
         int8_t *ve = ke + kTT;
-        int *vmax = reinterpret_cast<int *>(sc_s + j * a.sc_bytes + kTT * (1 + a.vpg));
+        int2 *v_range = reinterpret_cast<int2 *>(sc_s + j * a.sc_bytes + kTT * (1 + a.vpg));  // largest and least of each
         for (int s = 0; s < j && s < n_tiles; ++s) walker_advance<kTT>(w, a);
         uint32_t par = 0;
         const int per_page = a.page_size / a.sb;
@@ -449,15 +455,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) ke[lane + 32 * e] = (int8_t)kv8_exp(__ldg(a.k_scales + blk[e] * a.n_k + w.g));
             for (int v = 0; v < a.vpg; ++v) {
-                int m = kKv8MinExp;
+                int m = kKv8MinExp, lo = kKv8MaxExp;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int x = kv8_exp(__ldg(a.v_scales + blk[e] * a.n_v + min(v0 + v, a.n_v - 1)));
                     ve[v * kTT + lane + 32 * e] = (int8_t)x;
                     m = max(m, x);
+                    lo = min(lo, x);
                 }
                 m = __reduce_max_sync(0xffffffffu, m);
-                if (lane == 0) vmax[v] = m;
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                if (lane == 0) v_range[v] = make_int2(m, lo);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.sc_full[j]);
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             return (v * a.nb + h / 4 - first_block(a, g, QPK, v)) * 16 + h % 4 * 3;
         };
         float l[QPK];                    // this position's share of the row sums
-        float m_ref = 0.f, R = 0.f;      // lane h: head h's references (the same in the four warps)
+        float m_ref = 0.f, R = 0.f;      // lane h: head h's references, R less kTop (the same in the four warps)
         uint32_t vls[(QPK + 7) / 8] = {};  // V head of each query head inside the group, four bits each
         auto vl = [&](int h) { return (int)(vls[h >> 3] >> (4 * (h & 7)) & 15u); };
         int unit = -1, my_vl = 0;        // (lane h's own)
@@ -503,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float kf = exp2_int(ke[tid]);
             float vx[QPK];
 #pragma unroll
-            for (int h = 0; h < QPK; ++h) vx[h] = (float)ve[vl(h) * kTT + tid] + kTop;
-            const float vm = (float)reinterpret_cast<const int *>(sc_s + slot * a.sc_bytes + kTT * (1 + a.vpg))[my_vl];
+            for (int h = 0; h < QPK; ++h) vx[h] = (float)ve[vl(h) * kTT + tid];
+            const int2 v_range = reinterpret_cast<const int2 *>(sc_s + slot * a.sc_bytes + kTT * (1 + a.vpg))[my_vl];
             mbar_wait_bounded(&ms.s_full[k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             float s[QPK];
@@ -520,11 +528,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                     s[h] = tid < valid ? x * (ms.q_scale[unit & 1][h] * kf) : -INFINITY;
                 }
             }
-            // the tile's maxima: across the warp by redux, across the warps through shared memory
-            {
+            // vx: the logarithm of the whole weight, V scale included
+#pragma unroll
+            for (int h = 0; h < QPK; ++h) vx[h] += s[h];
+            // a tile's maxima: across the warp by redux, across the warps through shared memory
+            auto tile_max = [&](const float(&x)[QPK]) {
                 float m[QPK];
 #pragma unroll
-                for (int h = 0; h < QPK; ++h) m[h] = warp_max(s[h]);
+                for (int h = 0; h < QPK; ++h) m[h] = warp_max(x[h]);
                 if (lane == 0) {
 #pragma unroll
                     for (int h = 0; h < QPK; h += 4) {
@@ -536,15 +547,22 @@ __global__ void __launch_bounds__(kThreads, 2)
                             for (int e = 0; e < QPK; ++e) ms.red[k & 1][warp][e] = m[e];
                     }
                 }
-            }
-            named_barrier(1, kSoftmaxThreads);
+                named_barrier(1, kSoftmaxThreads);
+                const int h = lane < QPK ? lane : 0;
+                return fmaxf(fmax3f(ms.red[k & 1][0][h], ms.red[k & 1][1][h], ms.red[k & 1][2][h]), ms.red[k & 1][3][h]);
+            };
             // lane h moves head h's references where the tile exceeds them
             float alpha = 1.f, l_scale = 1.f;
             {
-                const int h = lane < QPK ? lane : 0;
-                const float mt = fmaxf(fmax3f(ms.red[k & 1][0][h], ms.red[k & 1][1][h], ms.red[k & 1][2][h]),
-                                       ms.red[k & 1][3][h]);
-                const float m_new = mt == -INFINITY ? 0.f : mt, r_new = m_new + vm;
+                const float top = tile_max(vx);
+                const float r_new = (top == -INFINITY ? (float)v_range.x : top) - kTop;
+                float m_new = r_new + (kTop - (float)v_range.x);
+                // (the same in all four warps) exponents too far apart for that: the scores' own maximum
+                if (__any_sync(0xffffffffu, lane < QPK && v_range.x - v_range.y > kSpread)) {
+                    named_barrier(1, kSoftmaxThreads);  // every warp has read the maxima
+                    const float m = tile_max(s);
+                    m_new = m == -INFINITY ? 0.f : m;
+                }
                 if (start) {
                     m_ref = m_new;
                     R = r_new;
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float m1 = __shfl_sync(0xffffffffu, m_ref, h1), r1 = __shfl_sync(0xffffffffu, R, h1);
                     l[h0] += fast_exp2(s[h0] - m0);
                     if (h1 > h0) l[h1] += fast_exp2(s[h1] - m1);
-                    split3x2(fast_exp2(s[h0] + (vx[h0] - r0)), fast_exp2(s[h1] + (vx[h1] - r1)), t[j]);
+                    split3x2(fast_exp2(vx[h0] - r0), fast_exp2(vx[h1] - r1), t[j]);
                 }
                 // (t[j][i]: term i of heads 2 j and 2 j + 1 of the block)  head 0: bytes 0-2, head 1: 3-5, head 2: 6-8, ...
                 pk[i].x = (t[0][0] & 0xffu) | (t[0][1] & 0xffu) << 8 | (t[0][2] & 0xffu) << 16 | (t[0][0] >> 8) << 24;
@@ -640,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                          __uint_as_float(r[0]));
                     const float m_h = __shfl_sync(0xffffffffu, m_ref, h), r_h = __shfl_sync(0xffffffffu, R, h);
                     const float l_h = ms.l_red[0][h] + ms.l_red[1][h] + ms.l_red[2][h] + ms.l_red[3][h];
-                    const float o_rel = o * exp2f(r_h - kTop - m_h);  // relative to 2^m
+                    const float o_rel = o * exp2f(r_h - m_h);  // relative to 2^m
                     if (whole) {
                         const long long row = (long long)w.b * a.n_q + w.g * QPK + h;
                         if (tid < DV && in_bounds(row, (long long)a.batch * a.n_q, a.status))
@@ -808,7 +826,7 @@ diffqkv_status_t decode_kv8_launch(const diffqkv_dims_t *d, const diffqkv_kv8_ca
     const uint32_t v_tile = (uint32_t)(kTT * d->d_v);
     const uint32_t p_bytes = (uint32_t)(ns * kTT), q_bytes = align_to((uint32_t)(ns * d->d_k), 1024);
     a.off_v = (uint32_t)(k_stages(d->d_k) * kTT * d->d_k);
-    a.sc_bytes = align_to((uint32_t)(kTT * (1 + span) + 4 * span), 16);
+    a.sc_bytes = align_to((uint32_t)(kTT * (1 + span) + 8 * span), 16);
     const uint32_t tail = 2 * p_bytes + 2 * q_bytes + kScaleWarps * a.sc_bytes + align_to((uint32_t)sizeof(Misc), 16);
     const uint32_t room = (per_sm == 2 ? 113u : 227u) * 1024 - 1024 - a.off_v - tail;
     a.v_slots = std::min<int>(kMaxVSlots, (int)(room / v_tile));

@@ -572,8 +572,9 @@ diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8
  * out[b,h] = sum_j softmax_j(scale q[b,h].k_j) v_j over the values k_j, v_j the cache
  * stands for.  The codes go to the tensor cores as they are; the query and the softmax
  * weights (times their V scales) are split into three e4m3 terms each: 12 significant
- * bits, or 2^-28 of the head's largest where that is more.  All sums, maxima and weights
- * are fp32.  Lengths, clamping, zero rows for length 0, max_seq_len, the workspace
+ * bits, or 2^-28 of the head's largest where that is more.  (The largest product of a
+ * position's own weight and V scale, that is: blocks of large scale and little weight
+ * cost the others nothing.)  All sums, maxima and weights are fp32.  Lengths, clamping, zero rows for length 0, max_seq_len, the workspace
  * (diffqkv_decode_workspace_size) and its error word are those of diffqkv_decode; entries
  * read, bad entries and shared pages those of diffqkv_decode_paged.
  */
