@@ -7,16 +7,19 @@
 //
 //  * One CTA takes 256 query rows of one request and head as two 128-row tiles that share every 64-position K/V tile
 //    (128-position tiles, whose S cannot be double-buffered in TMEM: 766 us where these take 500).  Four warps turn a
-//    tile's codes into f16 once for both: code * 2^(e - e_ref), with e_ref the tile's largest exponent for K and the
-//    largest so far for V, which is exact unless a block's scale is 2^15 below it.  (Feeding codes to fp8 MMAs instead
-//    would split every softmax weight into e4m3 terms, five more instructions for each pair of scores in the warps that
-//    bound this kernel; conversion costs the tile 12 instructions for 16 codes in warps that have nothing else to do.)
-//    K's e_ref goes into the scores' multiplier; when V's grows, O is rescaled.
+//    tile's codes into f16 once for both: code * 2^(e - e_ref), with e_ref the tile's largest exponent, exactly.  (Feeding
+//    codes to fp8 MMAs instead would split every softmax weight into e4m3 terms, five more instructions for each pair of
+//    scores in the warps that bound this kernel; conversion costs the tile 12 instructions for 16 codes in warps that have
+//    nothing else to do.)  K's e_ref goes into the scores' multiplier, V's into the weights' exponent.
+//  * O is held relative to 2^R, R a row's running maximum of (a tile's largest score + its V e_ref), the row sum relative to
+//    2^M, the largest score.  A tile whose exponents lie further apart (K: 2^15, beyond which f16 would round; V: 2^8,
+//    since R may be that much above every real weight) is `mixed`: codes are converted as they are, and the softmax
+//    applies each position's exponents, in fp32, with an exponential more a score.
 //  * Queries are scaled by a power of two per row into f16's range (8 significant bits fit its 11).
 //  * Softmax: two threads a row, 32 columns each, so that four warps a scheduler hide one another's latencies; S is
 //    double-buffered in TMEM, P (f16) goes back over S and is the A operand of P.V; O is rescaled in TMEM only when a
-//    row's maximum grows by 2^8 or V's exponent grows.  Weights are held at 2^7 of the reference, so that f16 resolves
-//    2^-31 of the largest; their sum is fp32, of the unrounded weights.
+//    row's R grows by 2^8.  Weights are held at 2^7 of the reference, so that f16 resolves 2^-31 of it, and of the largest
+//    weight 2^-23 at least; their sum is fp32, of the unrounded weights.
 //  * MMA, commit and TMA are issued by an elected lane (kv8.cuh).
 //  * Rows of Q come in, and rows of the output go out, with a row's 16-byte pieces in neighbouring lanes.
 //  * Units are taken longest first.  Where they are fewer than half of the SMs, each is cut into pieces of equal length, one
@@ -25,8 +28,7 @@
 //    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
 //    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
 // What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
-// their latencies.  Two prompts of 8192, 16 heads of 64/128: 485 us, 850 TFLOP/s, 0.50 of the measured GEMM peak (tensor
-// pipe 39% busy, XU 53%, 59% of issue slots); four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 505 us, 817 TFLOP/s, 0.49 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
 // one CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -48,10 +50,16 @@ constexpr int kLoadWarp = 16, kMmaWarp = 17, kScaleWarp = 18, kConvWarp0 = 19, k
 constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kRaw = 4;         // stages of codes
 constexpr int kScaleSlots = 8;  // tiles of scales, fetched four at a time
+constexpr int kExpSlots = 16;   // tiles of exponents that the softmax may still read
 constexpr int kSlots = 160;     // partial records of the workspace: one for each piece of a call whose units are cut
 constexpr int kCutBatch = 32;   // requests, at most, of a call whose units are cut
-constexpr float kRescale = 8.f;  // growth (log2) of a row's maximum before O is rescaled
+constexpr float kRescale = 8.f;  // growth (log2) of R before O is rescaled: weights stay below 2^(kShift + kRescale), inside f16
 constexpr float kShift = 7.f;    // weights are held at 2^kShift of the reference
+constexpr float kGrow = 40.f;    // growth of the largest score before the row sum is rescaled, where R does not ask for it
+constexpr float kFloor = 80.f;   // weights of a tile whose V is this far below the row's: 2^(kShift + kGrow - kFloor) at most,
+                                 // zero in f16, and still normal in fp32, for the row sum, down to 2^-53 of the largest
+constexpr int kSpreadK = 15, kSpreadV = 8;  // of a tile's exponents, above which it is mixed
+constexpr float kMixed = 0x1p120f;          // stands for V's e_ref of such a tile: above every R, so that the vote is for it
 
 struct PreArgs {
     const __nv_bfloat16 *q;
@@ -96,9 +104,12 @@ struct Misc {
     uint64_t raw_full[kRaw], raw_empty[kRaw], cv_full[3], cv_empty[3], sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint64_t q_full, s_full[QT][2], p_full[QT][2], pv_done[QT][2], mma_done;
     uint32_t k_mul[kScaleSlots][BN], v_mul[kScaleSlots][BN];  // 2^(e - e_ref) as f16 pairs, 0 behind the sequence
-    int k_ref[kScaleSlots], v_ref[kScaleSlots];               // e_ref
-    int ref[4][2];  // the same for the softmax, tile k in slot k & 3: K, V
-    float row_s[QT][2][BM];                                   // exchange between the two halves of a row
+    float2 scale_ref[kScaleSlots];  // 2^(e_ref) of K and e_ref of V, or kMixed
+    float2 ref[4];                  // the same for the softmax, tile k in slot k & 3
+    // K's and V's exponents of mixed tiles, tile k in slot k % kExpSlots.  (Tile k's are written when k - kScaleSlots
+    // has been converted, and so at least k - kScaleSlots - 3 been multiplied.)
+    alignas(16) char2 exps[kExpSlots][BN];
+    float row_s[QT][2][BM], row_y[QT][2][BM];                 // exchange between the two halves of a row
     int found[8];  // unit: request, block, q row, rows, length; its pieces, which of them, its first record
     uint32_t tmem_slot;
     int abort_flag, last_flag;
@@ -186,6 +197,68 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
         : "r"(id), "r"((uint32_t)x)
         : "memory");
     return r != 0;
+}
+
+// Factor of a row's products with keys of scale k: scale * log2(e) * 2^(the query's exponent) * k.  (A zero would turn masked
+// scores into NaN; NaN stays.)
+__device__ __forceinline__ float score_factor(float sc_row, float k) {
+    const float x = sc_row * k;
+    return x < 0x1p-126f ? 0x1p-126f : x;
+}
+
+// Half of a row of a mixed tile: its 32 columns of S and their positions' exponents, the columns that the row sees (0 .. last),
+// the row's factor.  Read eight columns at a time, twice, and out of line: in the softmax loop it took two prompts of 8192,
+// none of whose tiles is mixed, from 496 to 569 us, out of line to 505.  (All tiles mixed: 2290 us.)
+struct MixedHalf {
+    uint32_t t_s;
+    const char2 *exps;
+    int last;
+    float sc_row;
+};
+__device__ __forceinline__ void mixed_scores(const MixedHalf &x, int c, float (&s)[8], float (&ve)[8]) {
+    uint32_t z[8];
+    tmem_ld_cols<8>(x.t_s + (uint32_t)c, z);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const char2 ex = x.exps[c + e];
+        s[e] = c + e > x.last ? -INFINITY : __uint_as_float(z[e]) * score_factor(x.sc_row, exp2_int(ex.x));
+        ve[e] = (float)ex.y;
+    }
+}
+// Largest score, and score plus V exponent.
+__device__ __noinline__ float2 mixed_max(const MixedHalf x) {
+    float m = -INFINITY, y = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8) {
+        float s[8], ve[8];
+        mixed_scores(x, c, s, ve);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            m = fmaxf(m, s[e]);
+            y = fmaxf(y, s[e] + ve[e]);
+        }
+    }
+    return make_float2(m, y);
+}
+// Weights 2^(s + ve - R + 7) to the columns of P at t_p; returns l and their sum relative to 2^M.  The second half's weights
+// go over columns of the first half's scores.
+__device__ __noinline__ float mixed_weights(const MixedHalf x, float M, float R, float l, int half, int bar, uint32_t t_p) {
+    if (half == 1) named_barrier(bar, 64);
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8) {
+        float s[8], ve[8];
+        uint32_t pk[4];
+        mixed_scores(x, c, s, ve);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            l += fast_exp2(s[e] - M) + fast_exp2(s[e + 1] - M);
+            pk[e >> 1] = pack_f16x2(fast_exp2(s[e] + (ve[e] + kShift - R)), fast_exp2(s[e + 1] + (ve[e + 1] + kShift - R)));
+        }
+        tmem_st_cols<4>(t_p + (uint32_t)(c / 2), pk);
+    }
+    if (half == 0) named_barrier(bar, 64);
+    return l;
 }
 
 // The rows of a unit from the records of its pieces, in the order of its tiles.  A thread takes kItems (row, four columns)
@@ -462,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kScaleWarp) {
         // ======================= scales, four tiles at a time: lane l looks after positions 2 l and 2 l + 1 of a tile
         const int per_page = a.page_size / a.sb;
-        int v_run = kKv8MinExp;
         for (int n = n0; n < n1; n += 4) {
             int ek[4][2], ev[4][2];
 #pragma unroll
@@ -486,25 +558,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait_bounded(&ms.sc_empty[slot], (uint32_t)((k / kScaleSlots - 1) & 1), a.wait_limit_ns, abort_flag,
                                       a.status);
                 const int k0 = kv8_exp(ek[i][0]), k1 = kv8_exp(ek[i][1]), v0 = kv8_exp(ev[i][0]), v1 = kv8_exp(ev[i][1]);
-                const int kr = __reduce_max_sync(0xffffffffu, max(k0, k1));
-                const int vr = max(v_run, __reduce_max_sync(0xffffffffu, max(v0, v1)));
-                v_run = vr;
-                // 2^d in f16 for both halves of a word (2^-24 is its least; 0 is kept for positions behind the end)
+                int kr = __reduce_max_sync(0xffffffffu, max(k0, k1)), vr = __reduce_max_sync(0xffffffffu, max(v0, v1));
+                const bool mixed = kr - __reduce_min_sync(0xffffffffu, min(k0, k1)) > kSpreadK ||
+                                   vr - __reduce_min_sync(0xffffffffu, min(v0, v1)) > kSpreadV;
+                // 2^(e - ref) in f16 for both halves of a word, 1 in a mixed tile; 0 for positions behind the end
                 auto mul = [&](int e, int ref, int pos) -> uint32_t {
-                    if (pos >= T) return 0u;
-                    const int d = max(e - ref, -24);
-                    const uint32_t hbits = d >= -14 ? (uint32_t)(d + 15) << 10 : 1u << (d + 24);
-                    return hbits * 0x10001u;
+                    const int d = mixed ? 0 : e - ref;  // (2^-15 is the one that is subnormal)
+                    return pos >= T ? 0u : (d >= -14 ? (uint32_t)(d + 15) << 10 : 0x200u) * 0x10001u;
                 };
                 const int p = (n + i) * BN + 2 * lane;
                 ms.k_mul[slot][2 * lane] = mul(k0, kr, p);
                 ms.k_mul[slot][2 * lane + 1] = mul(k1, kr, p + 1);
                 ms.v_mul[slot][2 * lane] = mul(v0, vr, p);
                 ms.v_mul[slot][2 * lane + 1] = mul(v1, vr, p + 1);
-                if (lane == 0) {
-                    ms.k_ref[slot] = kr;
-                    ms.v_ref[slot] = vr;
+                if (mixed) {
+                    ms.exps[k % kExpSlots][2 * lane] = make_char2((signed char)k0, (signed char)v0);
+                    ms.exps[k % kExpSlots][2 * lane + 1] = make_char2((signed char)k1, (signed char)v1);
                 }
+                if (lane == 0) ms.scale_ref[slot] = make_float2(exp2_int(kr), mixed ? kMixed : (float)vr);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.sc_full[slot]);
             }
@@ -526,10 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool tail = (n0 + k + 1) * BN > T;
             widen_k.run(raw, dst, ms.k_mul[slot], tail);
             widen_v.run(raw + C::RAW_K, dst + C::K_BYTES, ms.v_mul[slot], tail);
-            if (ct == 0) {
-                ms.ref[k & 3][0] = ms.k_ref[slot];
-                ms.ref[k & 3][1] = ms.v_ref[slot];
-            }
+            if (ct == 0) ms.ref[k & 3] = ms.scale_ref[slot];
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
@@ -660,9 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.q_full);
         }
-        float m_used = 0.f;  // log2 maximum that O and l are relative to (the same in both halves)
-        float l = 0.f;       // this half's sum of the weights, 2^7 included
-        int v_run = 0;       // V exponent that O is relative to
+        float R = 0.f;       // O holds the sum of 2^(s - R + 7) v (R and M: the same in both halves)
+        float M = 0.f;       // l is relative to 2^M
+        float l = 0.f;       // this half's sum of the weights
         for (int n = n0; n < end[t]; ++n) {
             const int k = n - n0;
             const uint32_t t_s = tmem + (uint32_t)(t * 2 * BN + (k & 1) * BN) + lane_base;
@@ -672,9 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(t_s + (uint32_t)(half * 32), x);
             // (written before the tile's conversion was handed over, and so before its S; the slot is written again after
             // the P.V of tile k + 1)
-            const int k_ref = ms.ref[k & 3][0], v_ref = ms.ref[k & 3][1];
-            float sc = sc_row * exp2_int(k_ref);
-            if (sc < 0x1p-126f) sc = 0x1p-126f;  // (a zero would turn masked scores into NaN)
+            const float2 ref = ms.ref[k & 3];
+            const float sc = score_factor(sc_row, ref.x);
             tmem_wait_ld();
             const int j0 = n * BN + half * 32;
             if (j0 + 31 > first + row0 + t * BM) {  // causal mask, on columns that reach past the tile's first row
@@ -690,59 +757,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 8; e < 32; e += 8)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) m4[c] = fmax3f(m4[c], sv(e + c), sv(e + 4 + c));
-            const float m_half = fmaxf(fmax3f(m4[0], m4[1], m4[2]), m4[3]) * sc;
+            float m_half = fmaxf(fmax3f(m4[0], m4[1], m4[2]), m4[3]) * sc, y_half = m_half + ref.y;
             // Both halves have read S behind this barrier (P goes over columns of the other half), and agree on whether a
-            // reference has to move: the first tile, a row that grew by 2^8, a larger V exponent
-            const bool v_grow = v_ref > v_run;
-            if (pair_any(bar, k == 0 || v_grow || m_half > m_used + kRescale)) {
-                ms.row_s[t][half][r] = m_half;
-                named_barrier(bar, 64);
-                const float m_new = fmaxf(m_half, ms.row_s[t][1 - half][r]);
-                named_barrier(bar, 64);
-                if (k == 0) {
-                    m_used = m_new == -INFINITY ? 0.f : m_new;
-                    v_run = v_ref;
-                } else {
-                    // (S of tile k has been waited for, so P.V of tiles up to k - 2 is done: k - 1 is this barrier's next phase)
-                    mbar_wait_bounded(&ms.pv_done[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
-                                      a.status);
-                    tc_fence_after();
-                    const bool grow = m_new > m_used + kRescale;
-                    const float lf = grow ? fast_exp2(m_used - m_new) : 1.f;
-                    const float alpha = v_grow ? lf * fast_exp2((float)(v_run - v_ref)) : lf;
+            // reference has to move: the first tile, a row whose R grew by 2^8, a row sum that would leave its range, a mixed tile.
+            // (Two warps none of whose rows see any of a mixed tile may go on without: all of their weights are zero.)
+            do {
+                if (pair_any(bar, k == 0 || y_half > R + kRescale || m_half > M + kGrow)) {
+                    const MixedHalf mix{t_s + (uint32_t)(half * 32), ms.exps[k % kExpSlots] + half * 32, i - j0, sc_row};
+                    if (ref.y == kMixed) {
+                        const float2 my = mixed_max(mix);
+                        m_half = my.x;
+                        y_half = my.y;
+                    }
+                    ms.row_s[t][half][r] = m_half;
+                    ms.row_y[t][half][r] = y_half;
+                    named_barrier(bar, 64);
+                    const float m_new = fmaxf(m_half, ms.row_s[t][1 - half][r]), y_new = fmaxf(y_half, ms.row_y[t][1 - half][r]);
+                    named_barrier(bar, 64);
+                    if (k == 0) {
+                        M = m_new == -INFINITY ? 0.f : m_new;
+                        R = y_new == -INFINITY ? 0.f : y_new;
+                    } else {
+                        // (S of tile k has been waited for, so P.V of tiles up to k - 2 is done: k - 1 is this barrier's next phase)
+                        mbar_wait_bounded(&ms.pv_done[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
+                                          a.status);
+                        tc_fence_after();
+                        const bool grow = y_new > R + kRescale;
+                        const float alpha = grow ? fast_exp2(R - y_new) : 1.f;
+                        if (grow) R = y_new;
+                        if (m_new > M) {  // (with R, so that R - M stays an exponent of V)
+                            l *= fast_exp2(M - m_new);
+                            M = m_new;
+                        }
 #pragma unroll 1
-                    for (int c = 0; c < HV; c += 16) {
-                        uint32_t y[16];
-                        tmem_ld_cols<16>(t_o + c, y);
-                        tmem_wait_ld();
+                        for (int c = 0; c < HV; c += 16) {
+                            uint32_t y[16];
+                            tmem_ld_cols<16>(t_o + c, y);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
-                        tmem_st_cols<16>(t_o + c, y);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                            tmem_st_cols<16>(t_o + c, y);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
-                    if (grow) {
-                        l *= lf;
-                        m_used = m_new;
+                    if (ref.y == kMixed) {
+                        l = mixed_weights(mix, M, R, l, half, bar, t_s + (uint32_t)(half * 16));
+                        break;
                     }
-                    if (v_grow) v_run = v_ref;
                 }
-            }
-            // weights 2^(s - m + 7)
-            const f32x2_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(kShift - m_used, kShift - m_used);
-            uint32_t pk[16];
-            f32x2_t l2[2] = {0ull, 0ull};
+                uint32_t pk[16];
+                // weights 2^(s + e_ref - R + 7).  Where V's exponent is so far below the row's that they are zero in f16, larger
+                // ones that still are, lest they vanish from the sum
+                const float c = fmaxf(ref.y - R, -kFloor - M) + kShift;
+                const f32x2_t sc2 = f2_pack(sc, sc), c2 = f2_pack(c, c);
+                f32x2_t l2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float t0, t1;
-                f2_unpack(f2_fma(f2_pack(sv(e), sv(e + 1)), sc2, nm2), t0, t1);
-                const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
-                l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(p0, p1));
-                pk[e >> 1] = pack_f16x2(p0, p1);
-            }
-            tmem_st_cols<16>(t_s + (uint32_t)(half * 16), pk);
-            float la, lb;
-            f2_unpack(f2_add(l2[0], l2[1]), la, lb);
-            l += la + lb;
+                for (int e = 0; e < 32; e += 2) {
+                    float t0, t1;
+                    f2_unpack(f2_fma(f2_pack(sv(e), sv(e + 1)), sc2, c2), t0, t1);
+                    const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                    l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(p0, p1));
+                    pk[e >> 1] = pack_f16x2(p0, p1);
+                }
+                float la, lb;
+                f2_unpack(f2_add(l2[0], l2[1]), la, lb);
+                l = fmaf(la + lb, fast_exp2(-c - M), l);
+                tmem_st_cols<16>(t_s + (uint32_t)(half * 16), pk);
+            } while (false);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -757,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ms.row_s[t][half][r] = l;
         named_barrier(bar, 64);
         l += ms.row_s[t][1 - half][r];
-        const float o_scale = exp2f((float)v_run);  // (l carries the weights' 2^7 as O does)
+        const float o_scale = exp2f(R - kShift - M);
         // A whole unit: the rows, divided by their sums.  Otherwise this piece's record: O relative to m, four columns of all
         // rows after another, then (m, l) of the rows.
         const bool whole = pieces == 1;
@@ -803,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) {
             if (live && half == 0)
                 __stcg(reinterpret_cast<float2 *>(a.partials + (size_t)(record + piece) * C::REC + (size_t)DV * kRows) + t * BM + r,
-                       some ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f));
+                       some ? make_float2(M, l) : make_float2(-INFINITY, 0.f));
             __threadfence();
         }
     }

@@ -605,10 +605,12 @@ size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
  * descending, and n_b > seq_lens[b] are clamped and flagged DIFFQKV_ERR_DEVICE_SEQLEN in the
  * workspace's error word; a row without a position gets zeros.  Bad table entries as in
  * diffqkv_prefill_causal_paged.  Codes and queries are converted to f16 with power-of-two
- * scales (exactly, but for blocks whose scale is 2^15 below the largest of their tile of
- * 64 positions, for K, or of the sequence so far, for V), products are summed in fp32, and
- * softmax weights are rounded to f16 for the second product.  A NaN in a stored V row can
- * also reach rows up to 255 before it (a weight of zero times NaN).
+ * scales (exactly, but for elements of a query row 2^31 below its largest), products are
+ * summed in fp32, and softmax weights, their V scales included, are rounded to f16 for the
+ * second product: 11 significant bits, or multiples of 2^-23 of the row's largest where
+ * that is coarser.  (Tiles of 64 positions whose blocks' scales lie 2^9 apart, for V, or
+ * 2^16, for K, take about five times as long.)  A NaN in a stored V row can also reach
+ * rows up to 255 before it (a weight of zero times NaN).
  * tokens >= 1.  workspace as above.
  */
 diffqkv_status_t diffqkv_prefill_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
