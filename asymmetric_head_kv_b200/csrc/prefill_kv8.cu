@@ -28,7 +28,7 @@
 //    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
 //    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
 // What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
-// their latencies.  Two prompts of 8192, 16 heads of 64/128: 505 us, 817 TFLOP/s, 0.49 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 491 us, 840 TFLOP/s, 0.50 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
 // one CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -86,6 +86,29 @@ __device__ __forceinline__ int clamp_to(int v, int hi) { return min(max(v, 0), h
 __device__ __forceinline__ int2 request_rows(const PreArgs &a, int b) {
     const int s = clamp_to(__ldg(a.query_start + b), a.tokens), e = clamp_to(__ldg(a.query_start + b + 1), a.tokens);
     return make_int2(s, max(0, e - s));
+}
+
+// mbar_wait_bounded with what follows a failed first try out of line: a dozen copies of that loop among the roles' code cost
+// two prompts of 8192 3% (504 against 491 us).
+__device__ __noinline__ bool wait_on(uint32_t a, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag, int32_t *status) {
+    if (abort_flag && *abort_flag) return false;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(a, parity)) return true;
+        if ((n & 63u) == 0) {
+            if (abort_flag && *abort_flag) return false;
+            if (globaltimer_ns() - t0 > limit_ns) {
+                if (abort_flag) *abort_flag = 1;
+                record_error(status, DIFFQKV_ERR_DEVICE_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag,
+                                         int32_t *status) {
+    const uint32_t a = smem_addr(bar);
+    return mbar_try_wait(a, parity) || wait_on(a, parity, limit_ns, abort_flag, status);
 }
 
 template <int DK, int DV>
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int cnt = uniform(subs(n)), p = n * BN + lane * a.sub_rows;
             const int row = p - div_page(a, p) * a.page_size;
             if (n + 1 < n1) next = entry(n + 1);
-            if (issued >= kRaw) mbar_wait_bounded(&ms.raw_empty[st], par ^ 1u, a.wait_limit_ns, abort_flag, a.status);
+            if (issued >= kRaw) wait_for(&ms.raw_empty[st], par ^ 1u, a.wait_limit_ns, abort_flag, a.status);
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             if (elect_one()) mbar_arrive_expect_tx(&ms.raw_full[st], (uint32_t)(cnt * a.sub_rows * (DK + DV)));
             __syncwarp();
@@ -531,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         for (int k = max(0, issued - kRaw); k < issued; ++k)  // drain
-            mbar_wait_bounded(&ms.raw_full[k % kRaw], (uint32_t)(k / kRaw & 1), a.wait_limit_ns, nullptr, a.status);
+            wait_for(&ms.raw_full[k % kRaw], (uint32_t)(k / kRaw & 1), a.wait_limit_ns, nullptr, a.status);
     } else if (warp == kScaleWarp) {
         // ======================= scales, four tiles at a time: lane l looks after positions 2 l and 2 l + 1 of a tile
         const int per_page = a.page_size / a.sb;
@@ -555,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n + i >= n1) break;
                 const int k = n + i - n0, slot = k % kScaleSlots;
                 if (k >= kScaleSlots)
-                    mbar_wait_bounded(&ms.sc_empty[slot], (uint32_t)((k / kScaleSlots - 1) & 1), a.wait_limit_ns, abort_flag,
+                    wait_for(&ms.sc_empty[slot], (uint32_t)((k / kScaleSlots - 1) & 1), a.wait_limit_ns, abort_flag,
                                       a.status);
                 const int k0 = kv8_exp(ek[i][0]), k1 = kv8_exp(ek[i][1]), v0 = kv8_exp(ev[i][0]), v1 = kv8_exp(ev[i][1]);
                 int kr = __reduce_max_sync(0xffffffffu, max(k0, k1)), vr = __reduce_max_sync(0xffffffffu, max(v0, v1));
@@ -589,9 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t rp = 0, cp = 0;
         for (int k = 0; k < n1 - n0; ++k) {
             const int slot = k % kScaleSlots;
-            mbar_wait_bounded(&ms.sc_full[slot], (uint32_t)(k / kScaleSlots & 1), a.wait_limit_ns, abort_flag, a.status);
-            mbar_wait_bounded(&ms.raw_full[rs], rp, a.wait_limit_ns, abort_flag, a.status);
-            if (k >= C::STAGES) mbar_wait_bounded(&ms.cv_empty[cs], cp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
+            wait_for(&ms.sc_full[slot], (uint32_t)(k / kScaleSlots & 1), a.wait_limit_ns, abort_flag, a.status);
+            wait_for(&ms.raw_full[rs], rp, a.wait_limit_ns, abort_flag, a.status);
+            if (k >= C::STAGES) wait_for(&ms.cv_empty[cs], cp ^ 1u, a.wait_limit_ns, abort_flag, a.status);
             const uint8_t *raw = smem + C::OFF_RAW + rs * C::RAW;
             uint8_t *dst = smem + C::OFF_CONV + cs * C::CONV;
             const bool tail = (n0 + k + 1) * BN > T;
@@ -620,14 +643,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
         const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + C::OFF_CONV), 16, 1024);
         const uint64_t v_desc = smem_desc_sw128(smem_addr(smem + C::OFF_CONV + C::K_BYTES), BN * 128, 1024);
-        mbar_wait_bounded(&ms.q_full, 0, a.wait_limit_ns, abort_flag, a.status);
+        wait_for(&ms.q_full, 0, a.wait_limit_ns, abort_flag, a.status);
         tc_fence_after();
         int cs = 0, pst = 0;  // stage of tile n, of tile n - 1
         uint32_t cp = 0;
         for (int n = n0; n <= n1; ++n) {
             const int k = n - n0;
             if (n < n1) {
-                mbar_wait_bounded(&ms.cv_full[cs], cp, a.wait_limit_ns, abort_flag, a.status);
+                wait_for(&ms.cv_full[cs], cp, a.wait_limit_ns, abort_flag, a.status);
                 tc_fence_after();
                 const uint64_t kd = k_desc + (uint32_t)(cs * (C::CONV >> 4));
 #pragma unroll
@@ -652,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
                     if (n - 1 >= end[t]) continue;
-                    mbar_wait_bounded(&ms.p_full[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
+                    wait_for(&ms.p_full[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
                     tc_fence_after();
                     const uint32_t t_p = tmem + (uint32_t)(t * 2 * BN + ((k - 1) & 1) * BN);
                     if (elect_one()) {
@@ -675,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) umma_commit(&ms.mma_done);
         __syncwarp();
-        mbar_wait_bounded(&ms.mma_done, 0, a.wait_limit_ns, nullptr, a.status);
+        wait_for(&ms.mma_done, 0, a.wait_limit_ns, nullptr, a.status);
     } else {
         // ======================= softmax: warps 8 t .. 8 t + 7 hold query tile t; a row (TMEM lane r) belongs to two threads,
         // one for each half of a tile's columns.  Four warps a scheduler hide one another's latencies.
@@ -734,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = n0; n < end[t]; ++n) {
             const int k = n - n0;
             const uint32_t t_s = tmem + (uint32_t)(t * 2 * BN + (k & 1) * BN) + lane_base;
-            mbar_wait_bounded(&ms.s_full[t][k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
+            wait_for(&ms.s_full[t][k & 1], (uint32_t)(k >> 1 & 1), a.wait_limit_ns, abort_flag, a.status);
             tc_fence_after();
             uint32_t x[32];
             tmem_ld32(t_s + (uint32_t)(half * 32), x);
@@ -779,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         R = y_new == -INFINITY ? 0.f : y_new;
                     } else {
                         // (S of tile k has been waited for, so P.V of tiles up to k - 2 is done: k - 1 is this barrier's next phase)
-                        mbar_wait_bounded(&ms.pv_done[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
+                        wait_for(&ms.pv_done[t][(k - 1) & 1], (uint32_t)((k - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
                                           a.status);
                         tc_fence_after();
                         const bool grow = y_new > R + kRescale;
@@ -831,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int done = end[t] - n0;
         if (done > 0) {
-            mbar_wait_bounded(&ms.pv_done[t][(done - 1) & 1], (uint32_t)((done - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
+            wait_for(&ms.pv_done[t][(done - 1) & 1], (uint32_t)((done - 1) >> 1 & 1), a.wait_limit_ns, abort_flag,
                               a.status);
             tc_fence_after();
         }
