@@ -20,6 +20,10 @@
 //    double-buffered in TMEM, P (f16) goes back over S and is the A operand of P.V; O is rescaled in TMEM only when a
 //    row's R grows by 2^8.  Weights are held at 2^7 of the reference, so that f16 resolves 2^-31 of it, and of the largest
 //    weight 2^-23 at least; their sum is fp32, of the unrounded weights.
+//  * A weight of zero times a NaN is NaN, so a NaN code of V would reach rows before it in the tiles on the diagonal.  There the
+//    warp that fetches the scales looks the codes over before it hands the tile on, puts zeros in the place of NaN and notes
+//    each column's first one; the rows from that position on get their NaN with the output.  (Two prompts of 8192: 491 us
+//    without, 493 so; 542 with the look at the codes inline, 523 with it in the conversion warps, 510 in a warp of its own.)
 //  * MMA, commit and TMA are issued by an elected lane (kv8.cuh).
 //  * Rows of Q come in, and rows of the output go out, with a row's 16-byte pieces in neighbouring lanes.
 //  * Units are taken longest first.  Where they are fewer than half of the SMs, each is cut into pieces of equal length, one
@@ -28,7 +32,7 @@
 //    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
 //    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
 // What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
-// their latencies.  Two prompts of 8192, 16 heads of 64/128: 491 us, 840 TFLOP/s, 0.50 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 493 us, 837 TFLOP/s, 0.50 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
 // one CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -43,7 +47,7 @@ namespace diffqkv {
 
 namespace {
 
-constexpr int BM = 128, QT = 2, BN = 64;
+constexpr int BM = 128, QT = 2, BN = 64, DV_MAX = 128;
 constexpr int kRows = QT * BM;
 constexpr int kSoftmaxWarps = 8 * QT;  // two warps per 32 rows, 32 columns of S each
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kScaleWarp = 18, kConvWarp0 = 19, kConvWarps = 4;
@@ -133,6 +137,7 @@ struct Misc {
     // has been converted, and so at least k - kScaleSlots - 3 been multiplied.)
     alignas(16) char2 exps[kExpSlots][BN];
     float row_s[QT][2][BM], row_y[QT][2][BM];                 // exchange between the two halves of a row
+    int nan_pos[DV_MAX], nan_seen;  // first position with a NaN of each column of V, on the diagonal; whether there is one
     int found[8];  // unit: request, block, q row, rows, length; its pieces, which of them, its first record
     uint32_t tmem_slot;
     int abort_flag, last_flag;
@@ -207,6 +212,32 @@ struct Widen {
         }
     }
 };
+
+// NaN in a V tile of codes, rows of DV bytes, the first at position `pos` (one warp): zeros in their place, and their columns'
+// least positions in `first`.
+template <int DV>
+__device__ __noinline__ void take_nans(uint8_t *tile, int pos, int lane, int *first, int *seen) {
+    auto nan4 = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };  // (codes 0x7f and 0xff)
+#pragma unroll 1
+    for (int i = lane * 16; i < BN * DV; i += 4 * 32 * 16) {
+        uint4 c[4];
+        uint32_t any = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = lds128(tile + i + k * (32 * 16));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) any |= nan4(c[k].x) | nan4(c[k].y) | nan4(c[k].z) | nan4(c[k].w);
+        if (!any) continue;
+        *seen = 1;
+#pragma unroll 1
+        for (int e = 0; e < 64; ++e) {
+            const int at = i + (e >> 4) * (32 * 16) + (e & 15);
+            if ((tile[at] & 0x7f) != 0x7f) continue;
+            tile[at] = 0;
+            atomicMin(first + at % DV, pos + at / DV);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 
 // Barrier of the two warps of `id`; true where the predicate holds in any of their threads.
 __device__ __forceinline__ bool pair_any(int id, bool x) {
@@ -397,10 +428,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.pv_done[t][1], 1);
         }
         mbar_init(&ms.mma_done, 1);
+        ms.nan_seen = 0;
         ms.abort_flag = 0;
         ms.last_flag = 0;
         fence_barrier_init();
     }
+    if (tid < DV) ms.nan_pos[tid] = 0x7fffffff;
     // ---- the piece: of a unit (256-row block, head), heaviest first: up to 32 requests by their length, more in the reverse
     // of their order; a request's last block (the longest context) first, the pieces of a block side by side
     if (warp == 0) {
@@ -599,6 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ms.exps[k % kExpSlots][2 * lane + 1] = make_char2((signed char)k1, (signed char)v1);
                 }
                 if (lane == 0) ms.scale_ref[slot] = make_float2(exp2_int(kr), mixed ? kMixed : (float)vr);
+                if ((n + i + 1) * BN - 1 > first + row0) {  // positions that not every row sees
+                    wait_for(&ms.raw_full[k % kRaw], (uint32_t)(k / kRaw & 1), a.wait_limit_ns, abort_flag, a.status);
+                    take_nans<DV>(smem + C::OFF_RAW + k % kRaw * C::RAW + C::RAW_K, (n + i) * BN, lane, ms.nan_pos, &ms.nan_seen);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.sc_full[slot]);
             }
@@ -880,6 +917,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(some ? __uint_as_float(y[e]) * inv_l * o_scale : 0.f);
+            if (ms.nan_seen) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (i >= ms.nan_pos[half * HV + c + e]) y[e] = 0x7fffffffu;
+            }
             if (whole) {
 #pragma unroll
                 for (int e = 0; e < 16; e += 2)

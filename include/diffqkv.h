@@ -609,8 +609,8 @@ size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
  * summed in fp32, and softmax weights, their V scales included, are rounded to f16 for the
  * second product: 11 significant bits, or multiples of 2^-23 of the row's largest where
  * that is coarser.  (Tiles of 64 positions whose blocks' scales lie 2^9 apart, for V, or
- * 2^16, for K, take about five times as long.)  A NaN in a stored V row can also reach
- * rows up to 255 before it (a weight of zero times NaN).
+ * 2^16, for K, take about five times as long.)  A NaN in a stored row reaches the query
+ * rows at and behind its position (of K: the heads' whole rows, of V: its column), no others.
  * tokens >= 1.  workspace as above.
  */
 diffqkv_status_t diffqkv_prefill_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
