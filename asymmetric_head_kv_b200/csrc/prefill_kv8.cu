@@ -32,7 +32,7 @@
 //    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
 //    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
 // What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
-// their latencies.  Two prompts of 8192, 16 heads of 64/128: 493 us, 837 TFLOP/s, 0.50 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 488 us, 845 TFLOP/s, 0.50 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
 // one CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -93,7 +93,8 @@ __device__ __forceinline__ int2 request_rows(const PreArgs &a, int b) {
 }
 
 // mbar_wait_bounded with what follows a failed first try out of line: a dozen copies of that loop among the roles' code cost
-// two prompts of 8192 3% (504 against 491 us).
+// two prompts of 8192 3% (504 against 491 us).  The TMA producer keeps it inline: five rows over 131072 positions, which its
+// requests bound, take 171 us so and 191 without.
 __device__ __noinline__ bool wait_on(uint32_t a, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag, int32_t *status) {
     if (abort_flag && *abort_flag) return false;
     const uint64_t t0 = globaltimer_ns();
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int cnt = uniform(subs(n)), p = n * BN + lane * a.sub_rows;
             const int row = p - div_page(a, p) * a.page_size;
             if (n + 1 < n1) next = entry(n + 1);
-            if (issued >= kRaw) wait_for(&ms.raw_empty[st], par ^ 1u, a.wait_limit_ns, abort_flag, a.status);
+            if (issued >= kRaw) mbar_wait_bounded(&ms.raw_empty[st], par ^ 1u, a.wait_limit_ns, abort_flag, a.status);
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             if (elect_one()) mbar_arrive_expect_tx(&ms.raw_full[st], (uint32_t)(cnt * a.sub_rows * (DK + DV)));
             __syncwarp();
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         for (int k = max(0, issued - kRaw); k < issued; ++k)  // drain
-            wait_for(&ms.raw_full[k % kRaw], (uint32_t)(k / kRaw & 1), a.wait_limit_ns, nullptr, a.status);
+            mbar_wait_bounded(&ms.raw_full[k % kRaw], (uint32_t)(k / kRaw & 1), a.wait_limit_ns, nullptr, a.status);
     } else if (warp == kScaleWarp) {
         // ======================= scales, four tiles at a time: lane l looks after positions 2 l and 2 l + 1 of a tile
         const int per_page = a.page_size / a.sb;
