@@ -123,6 +123,7 @@ __device__ __forceinline__ void store_run(const StoreArgs &a, const uint4 *x, ui
     constexpr int LPR = D / 8;              // lanes of a row (8 elements each)
     const int ROWS = G / LPR * share;       // rows of one load of the groups
     const int sub = mine * (G / LPR) + lane / LPR, part = lane % LPR;
+    if (!in_bounds(blk, a.slots / a.sb, a.status) || !in_bounds((long long)t0 + len - 1, a.tokens, a.status)) return;
     uint8_t *byte = scales + (size_t)blk * heads + head;
     const int old = low > 0 ? kv8_exp(*byte) : 0;
     auto row_of = [&](int i) { return x + ((size_t)(t0 + i) * heads + head) * LPR + part; };
@@ -176,13 +177,13 @@ __device__ __forceinline__ void store_run(const StoreArgs &a, const uint4 *x, ui
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-            if (base + v * ROWS < len)
+            if (base + v * ROWS < len && in_bounds(slot[v], a.slots, a.status))
                 *reinterpret_cast<uint2 *>(pages + ((size_t)slot[v] * heads + head) * D + part * 8) =
                     quantise8(keep[v], f);
     }
     if (low > 0 && e > old) {
         const float g = exp2_int(max(old - e, -126));  // 2^-126 already takes every code to zero
-        for (int r = sub; r < low; r += ROWS) {
+        for (int r = sub; r < low && in_bounds(r, a.sb, a.status); r += ROWS) {
             uint2 *p = reinterpret_cast<uint2 *>(pages + (((size_t)blk * a.sb + r) * heads + head) * D + part * 8);
             uint2 c = *p;
             c.x = move4(c.x, g);

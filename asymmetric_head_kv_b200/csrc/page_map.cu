@@ -84,6 +84,14 @@ __device__ __forceinline__ int checked_page(const PageMapArgs &a, int page) {
     return -1;
 }
 
+// Whether the table has an entry lp of request b (checked build).
+__device__ __forceinline__ bool in_table(const PageMapArgs &a, int b, int lp) {
+    return in_bounds(b, a.batch, a.status) && in_bounds(lp, a.max_blocks, a.status);
+}
+__device__ __forceinline__ int held_entry(const PageMapArgs &a, int b, int lp) {
+    return in_table(a, b, lp) ? a.block_table[(size_t)b * a.max_blocks + lp] : -1;
+}
+
 // ONE: at most THREADS requests, one a thread.
 // TOKENS: consecutive tokens of a thread.
 template <int THREADS, bool ONE, int TOKENS>
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
     }
     int own_page = -1;  // pool page of the position after the cached ones, where that page is held
     if (ONE && b0 < b1 && own.n > 0 && page_of(a, own.s) < own.have)
-        own_page = a.block_table[(size_t)b0 * a.max_blocks + page_of(a, own.s)];
+        own_page = held_entry(a, b0, page_of(a, own.s));
     long long it = t, ip = p;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -169,7 +177,10 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
         const int q = page_of(a, s);
         return q + (s != q * a.page_size);
     };
-    auto free_page = [&](int k) { return k < THREADS ? free_s[k] : __ldg(a.free_pages + k); };
+    auto free_page = [&](int k) {
+        if (!in_bounds(k, a.num_free, a.status)) return -1;
+        return k < THREADS ? free_s[k] : __ldg(a.free_pages + k);
+    };
 
     // table entries of the pages taken
     for (int k = blockIdx.x * THREADS + tid; k < pages; k += stride) {
@@ -179,13 +190,14 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
             have = held_pages(len_s[run]);
         } else {
             Request r = load_request(a, b, false, false);
-            while (k >= off + r.take) {
+            while (k >= off + r.take && in_bounds(b + 1, a.batch, a.status)) {
                 off += r.take;
                 r = load_request(a, ++b, false, false);
             }
             have = r.have;
         }
-        a.block_table[(size_t)b * a.max_blocks + have + (k - off)] = checked_page(a, free_page(k));
+        if (in_table(a, b, have + (k - off)))
+            a.block_table[(size_t)b * a.max_blocks + have + (k - off)] = checked_page(a, free_page(k));
     }
 
     // slots and positions, TOKENS consecutive tokens a thread
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
             for (int e = 0; e < TOKENS; ++e) {
                 const int i = (int)i0 + e;
                 if (i >= tokens) break;
-                while (i >= end) {
+                while (i >= end && in_bounds(b + 1, a.batch, a.status)) {
                     seen = -1;
                     if (ONE) {
                         b = ++run;
@@ -238,7 +250,7 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(const PageMapArgs a) 
                     seen = lp;
                     page = checked_page(a, lp >= have                  ? free_page(off + (lp - have))
                                            : ONE && lp == page_of(a, s) ? page_s[run]
-                                                                        : a.block_table[(size_t)b * a.max_blocks + lp]);
+                                                                        : held_entry(a, b, lp));
                 }
                 if (page >= 0) slot[e] = page * a.page_size + (pos[e] - lp * a.page_size);
             }

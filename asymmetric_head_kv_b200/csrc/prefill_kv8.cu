@@ -321,6 +321,9 @@ __device__ __noinline__ float mixed_weights(const MixedHalf x, float M, float R,
 template <int DV, int kItems, int kAhead>
 __device__ __forceinline__ void merge_pieces(const PreArgs &a, int record, int n, int q0, int rows, int h, int tid) {
     constexpr size_t kRec = (size_t)kRows * (DV + 2);
+    if (!in_bounds(record, kSlots, a.status) || !in_bounds(record + n - 1, kSlots, a.status) ||
+        !in_bounds(q0 + rows - 1, a.tokens, a.status))
+        return;
     // a warp: 8 rows by 4 fours of columns, whole sectors in the records (columns by fours ahead of rows) and in the output
     const int r8 = (rows + 7) >> 3, items = r8 * DV * 2;
     auto row_of = [&](int e) { return (e >> 5) % r8 * 8 + (e & 7); };
@@ -525,8 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n_all == 0 || n0 >= n1) {
         if (n_all == 0 && piece == 0)  // rows without a position
             for (int e = tid; e < min(n_rows - row0, kRows) * (DV / 8); e += kThreads)
-                *reinterpret_cast<uint4 *>(a.out + ((size_t)(q0 + e / (DV / 8)) * a.n_q + h) * DV + e % (DV / 8) * 8) =
-                    make_uint4(0, 0, 0, 0);
+                if (in_bounds(q0 + e / (DV / 8), a.tokens, a.status))
+                    *reinterpret_cast<uint4 *>(a.out + ((size_t)(q0 + e / (DV / 8)) * a.n_q + h) * DV + e % (DV / 8) * 8) =
+                        make_uint4(0, 0, 0, 0);
         return;
     }
     const int end[QT] = {min(n_kv[0], n1), min(n_kv[1], n1)};
@@ -942,13 +946,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-            } else if (live) {
+            } else if (live && in_bounds(record + piece, kSlots, a.status)) {
 #pragma unroll
                 for (int e = 0; e < 16; e += 4, rec += kRows) __stcg(rec, make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]));
             }
         }
         if (!whole) {
-            if (live && half == 0)
+            if (live && half == 0 && in_bounds(record + piece, kSlots, a.status))
                 __stcg(reinterpret_cast<float2 *>(a.partials + (size_t)(record + piece) * C::REC + (size_t)DV * kRows) + t * BM + r,
                        some ? make_float2(M, l) : make_float2(-INFINITY, 0.f));
             __threadfence();
@@ -965,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- a cut unit: the last of its CTAs merges the records
     if (tid == 0) {
         __threadfence();
-        ms.last_flag = atomicAdd(a.counters + record, 1u) == (unsigned)(pieces - 1);
+        ms.last_flag = in_bounds(record, kSlots, a.status) && atomicAdd(a.counters + record, 1u) == (unsigned)(pieces - 1);
     }
     __syncthreads();
     if (!*(volatile int *)&ms.last_flag) return;
