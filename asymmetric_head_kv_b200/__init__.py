@@ -415,7 +415,8 @@ def page_map(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
     that the new positions need, taken from the front of free_pages (int32) in the requests' order.  Returns
     (query_start [B + 1], slot_map [capacity], positions [capacity], total_lens [B], pages_used [1]), all int32;
     give them, or ``capacity`` (rows of the step's token buffer) to have them allocated.  A step that does not fit
-    ``capacity`` or ``free_pages`` is dropped as a whole and flagged (``diffqkv_page_map``)."""
+    ``capacity`` or ``free_pages`` is dropped as a whole and flagged (``diffqkv_page_map``).  Outputs must be buffers of
+    their own: total_lens given as seq_lens, for one, is refused."""
     i32 = torch.int32
     if slot_map is None or query_start is None or total_lens is None or pages_used is None:
         with _on(stream):

@@ -283,6 +283,24 @@ diffqkv_status_t page_map_launch(int32_t batch, const int32_t *seq_lens, const i
     for (const void *w : words)
         if (reinterpret_cast<uintptr_t>(w) & 3u) return DIFFQKV_ERR_MISALIGNED;
     if (!aligned16(slot_map) || !aligned16(positions)) return DIFFQKV_ERR_MISALIGNED;
+    // outputs apart from inputs and from one another: CTAs that redo the sums would read another one's results
+    struct Range {
+        const void *p;
+        long long words;
+    };
+    const Range in[] = {{seq_lens, batch}, {new_lens, batch}, {free_pages, num_free}};
+    const Range out[] = {{block_table, (long long)batch * max_blocks}, {query_start, batch + 1}, {slot_map, capacity},
+                         {positions, capacity}, {total_lens, batch}, {pages_used, 1}};
+    auto meet = [](const Range &x, const Range &y) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+        return x.p && y.p && a < b + 4 * (uintptr_t)y.words && b < a + 4 * (uintptr_t)x.words;
+    };
+    for (size_t i = 0; i < sizeof out / sizeof *out; ++i) {
+        for (const Range &x : in)
+            if (meet(out[i], x)) return DIFFQKV_ERR_INVALID_ARG;
+        for (size_t j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return DIFFQKV_ERR_INVALID_ARG;
+    }
     DeviceInfo dev;
     const diffqkv_status_t st = current_device_info(&dev);
     if (st != DIFFQKV_OK) return st;

@@ -499,8 +499,9 @@ diffqkv_status_t diffqkv_prefill_causal_paged(const diffqkv_dims_t *dims, const 
  * (DIFFQKV_ERR_DEVICE_PAGE) is dropped as a whole: no table entry is written, every
  * slot and position is -1, pages_used and query_start are 0 and total_lens are the
  * lengths held before.  A free or held page outside [0, num_pages) is flagged
- * DIFFQKV_ERR_DEVICE_PAGE and its tokens' slots are -1.  Outputs must not overlap inputs
- * (block_table aside) or one another.  One launch, no workspace; device_status_word as in
+ * DIFFQKV_ERR_DEVICE_PAGE and its tokens' slots are -1.  Outputs that overlap inputs or
+ * one another (total_lens given as seq_lens, say) are refused with
+ * DIFFQKV_ERR_INVALID_ARG.  One launch, no workspace; device_status_word as in
  * diffqkv_prefill_causal_ex.  max_blocks * page_size and num_pages * page_size must
  * fit in int32 and batch is at most 2^24 (else DIFFQKV_ERR_UNSUPPORTED); int32 arrays
  * 4-byte aligned unless stated.
