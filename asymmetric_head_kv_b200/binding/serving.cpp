@@ -128,6 +128,20 @@ float scale_arg(PyObject *o, int32_t d_k) {
     return static_cast<float>(s);
 }
 
+// Calls an entry point (its arguments are plain values by then) without the interpreter's lock: a launch can wait for a full
+// queue, and what it waits for can be a host function that wants the lock.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+};
+template <class F, class... A>
+diffqkv_status_t unlocked(F entry, A... args) {
+    const Unlocked u;
+    return entry(args...);
+}
+
 // Runs a call; nothing crosses into Python as a C++ exception.
 template <class F>
 PyObject *guarded(const void *entry, F f) {
@@ -162,13 +176,14 @@ PyObject *page_map(PyObject *, PyObject *const *o, Py_ssize_t n) {
         auto i32 = [&](int i, const char *name, at::IntArrayRef shape) {
             return static_cast<int32_t *>(address(o[i], name, at::kInt, shape, dev));
         };
-        return (g_page_map(
+        return unlocked(
+            g_page_map,
             size32(B, "seq_lens"), i32(0, "seq_lens", {B}), i32(1, "new_lens", {B}), i32(2, "block_table", {B, mb}),
             size32(mb, "block_table"), int_arg(o[4], "page_size"), int_arg(o[5], "num_pages"),
             i32(3, "free_pages", {free}), size32(free, "free_pages"), size32(cap, "slot_map"),
             i32(6, "query_start", {B + 1}), i32(7, "slot_map", {cap}),
             o[8] == Py_None ? nullptr : i32(8, "positions", {cap}), i32(9, "total_lens", {B}),
-            i32(10, "pages_used", {1}), status_word(o[11], dev), stream_of(o[12], dev)));
+            i32(10, "pages_used", {1}), status_word(o[11], dev), stream_of(o[12], dev));
     });
 }
 
@@ -180,10 +195,10 @@ PyObject *kv8_store(PyObject *, PyObject *const *o, Py_ssize_t n) {
         const int64_t T = tensor(o[2], "slot_map").numel();
         const int64_t n_q = static_cast<int64_t>(c.n_k) * c.n_v;
         const diffqkv_dims_t dims{1, size32(n_q, "k_pages"), c.n_k, c.n_v, c.d_k, c.d_v, 1.f};
-        return (g_store(&dims, &c.c, address(o[0], "k_new", at::kBFloat16, {T, c.n_k, c.d_k}, c.dev),
+        return unlocked(g_store, &dims, &c.c, address(o[0], "k_new", at::kBFloat16, {T, c.n_k, c.d_k}, c.dev),
                                        address(o[1], "v_new", at::kBFloat16, {T, c.n_v, c.d_v}, c.dev),
                                        static_cast<int32_t *>(address(o[2], "slot_map", at::kInt, {T}, c.dev)),
-                                       size32(T, "slot_map"), status_word(o[7], c.dev), stream_of(o[8], c.dev)));
+                                       size32(T, "slot_map"), status_word(o[7], c.dev), stream_of(o[8], c.dev));
     });
 }
 
@@ -198,13 +213,13 @@ PyObject *decode_paged_kv8(PyObject *, PyObject *const *o, Py_ssize_t n) {
         if (table.dim() != 2) value_error("block_table", "[B, max_blocks]");
         const int64_t B = q.size(0), n_q = q.size(1), mb = table.size(1);
         const diffqkv_dims_t dims{size32(B, "q"), size32(n_q, "q"), c.n_k, c.n_v, c.d_k, c.d_v, scale_arg(o[7], c.d_k)};
-        return (g_decode(
-            &dims, &c.c, address(o[0], "q", at::kBFloat16, {B, n_q, c.d_k}, c.dev),
+        return unlocked(
+            g_decode, &dims, &c.c, address(o[0], "q", at::kBFloat16, {B, n_q, c.d_k}, c.dev),
             static_cast<int32_t *>(address(o[5], "block_table", at::kInt, {B, mb}, c.dev)), size32(mb, "block_table"),
             static_cast<int32_t *>(address(o[6], "seq_lens", at::kInt, {B}, c.dev)), int_arg(o[8], "max_seq_len"),
             address(o[9], "out", at::kBFloat16, {B, n_q, c.d_v}, c.dev),
             address(o[10], "workspace", at::kByte, ws.sizes(), c.dev), static_cast<size_t>(ws.numel()),
-            stream_of(o[11], c.dev)));
+            stream_of(o[11], c.dev));
     });
 }
 
@@ -220,14 +235,14 @@ PyObject *prefill_paged_kv8(PyObject *, PyObject *const *o, Py_ssize_t n) {
         const int64_t T = q.size(0), n_q = q.size(1), B = table.size(0), mb = table.size(1);
         const diffqkv_dims_t dims{size32(B, "block_table"), size32(n_q, "q"), c.n_k, c.n_v, c.d_k, c.d_v,
                                   scale_arg(o[8], c.d_k)};
-        return (g_prefill(
-            &dims, &c.c, address(o[0], "q", at::kBFloat16, {T, n_q, c.d_k}, c.dev),
+        return unlocked(
+            g_prefill, &dims, &c.c, address(o[0], "q", at::kBFloat16, {T, n_q, c.d_k}, c.dev),
             static_cast<int32_t *>(address(o[1], "query_start", at::kInt, {B + 1}, c.dev)), size32(T, "q"),
             static_cast<int32_t *>(address(o[6], "block_table", at::kInt, {B, mb}, c.dev)), size32(mb, "block_table"),
             static_cast<int32_t *>(address(o[7], "seq_lens", at::kInt, {B}, c.dev)),
             address(o[9], "out", at::kBFloat16, {T, n_q, c.d_v}, c.dev),
             address(o[10], "workspace", at::kByte, ws.sizes(), c.dev), static_cast<size_t>(ws.numel()),
-            stream_of(o[11], c.dev)));
+            stream_of(o[11], c.dev));
     });
 }
 

@@ -32,3 +32,36 @@ for call, n in ((ext.page_map, 13), (ext.kv8_store, 9), (ext.decode_paged_kv8, 1
         print("refused")
 ''')
     assert out.split() == ["refused"] * 4
+
+
+@pytest.mark.gpu
+def test_other_threads_run_while_a_call_waits(cuda_device):
+    """An entry point that blocks (here libc's usleep, in the place of a launch that waits for a full queue) holds no
+    interpreter lock."""
+    out = _child('''
+import ctypes, threading, time
+import torch
+from asymmetric_head_kv_b200 import _serving as ext
+usleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+ext.bind(usleep, usleep, usleep, usleep)
+B = 400000  # usleep's argument, by page_map's first one
+z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+lens, table, one, start, slots = z(B), z(B).view(B, 1), z(1), z(B + 1), z(4)
+torch.cuda.synchronize()
+ticks, stop = [], threading.Event()
+def tick():
+    while not stop.is_set():
+        ticks.append(time.monotonic())
+        time.sleep(0.001)
+t = threading.Thread(target=tick)
+t.start()
+time.sleep(0.05)
+t0 = time.monotonic()
+assert ext.page_map(lens, lens, table, one, 16, 8, start, slots, None, lens, one, None, None) == 0
+t1 = time.monotonic()
+stop.set()
+t.join()
+print(t1 - t0, sum(t0 + 0.01 < x < t1 - 0.01 for x in ticks))
+''')
+    took, ticks = out.split()
+    assert float(took) > 0.35 and int(ticks) >= 20, out
