@@ -4,7 +4,10 @@ Usage: ``python -m asymmetric_head_kv_b200.build`` (or ``build()`` from Python).
 Each .cu file under csrc/ compiles to an object in _build/ (in parallel) and
 they link into asymmetric_head_kv_b200/libdiffqkv.so.  Recompiles only what
 changed (source or any header newer than its object).  The CPython extension that
-marshals the serving operators (binding/serving.cpp) is built with g++ next to it.
+marshals the serving operators (binding/serving.cpp) is built with g++ next to it, last,
+and again whenever it was built for another torch or Python than this one's.  The
+library needs neither: where g++ or the headers of Python or torch are missing, the
+build warns and leaves the extension out (the Python serving calls then say so).
 """
 from __future__ import annotations
 
@@ -15,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +28,7 @@ LIB = os.path.join(PKG, "libdiffqkv.so")
 LIB_CHECKED = os.path.join(PKG, "libdiffqkv_checked.so")
 BINDING_SRC = os.path.join(PKG, "binding", "serving.cpp")
 BINDING = os.path.join(PKG, "_serving.so")
+BINDING_KEY = os.path.join(BUILD, "serving.key")  # what the extension beside it was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -78,13 +83,46 @@ def _build_one(lib: str, objdir: str, force: bool, verbose: bool, extra_flags) -
     return lib
 
 
-def _build_binding(force: bool) -> str:
-    deps = [BINDING_SRC, os.path.join(ROOT, "include", "diffqkv.h"), __file__]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
-        return BINDING
-    import torch
+def _binding_key(torch) -> str:
+    """What an extension is good for: it reads tensors through inlined code of this torch, in this interpreter."""
+    return " ".join([torch.__version__, f"cxx11abi={int(torch.compiled_with_cxx11_abi())}",
+                     str(sysconfig.get_config_var("SOABI"))])
 
+
+def _missing_for_binding(torch_dir: str):
+    """The first thing that the extension's build needs and this machine lacks, or None."""
+    if shutil.which("g++") is None:
+        return "g++"
+    for f in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+              os.path.join(torch_dir, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        if not os.path.exists(f):
+            return f
+    return None
+
+
+def _build_binding(force: bool):
+    """The extension's path, or None (with a warning) where it cannot be built here."""
+    try:
+        import torch
+    except ImportError:
+        warnings.warn("torch is not installed: the serving operators' Python extension is left out")
+        return None
+    key = _binding_key(torch)
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "diffqkv.h"), __file__]
+    built_for = None
+    if os.path.exists(BINDING_KEY):
+        with open(BINDING_KEY) as f:
+            built_for = f.read()
+    if not force and os.path.exists(BINDING) and built_for == key and \
+            os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
     t = os.path.dirname(torch.__file__)
+    lacking = _missing_for_binding(t)
+    if lacking:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # (of other sources, or for another torch: better none)
+        warnings.warn(f"{lacking} is missing: the serving operators' Python extension is left out")
+        return None
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
@@ -96,6 +134,9 @@ def _build_binding(force: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for serving.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_KEY, "w") as f:
+        f.write(key)
     return BINDING
 
 
@@ -103,9 +144,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     """Builds libdiffqkv.so and, unless checked=False, libdiffqkv_checked.so: the same sources with
     -DDIFFQKV_BOUNDS_CHECK (device-side index checks; selected at run time by DIFFQKV_BOUNDS_CHECK=1)."""
     lib = _build_one(LIB, BUILD, force, verbose, extra_flags)
-    _build_binding(force)
     if checked:
         _build_one(LIB_CHECKED, BUILD + "_checked", force, verbose, tuple(extra_flags) + ("-DDIFFQKV_BOUNDS_CHECK",))
+    _build_binding(force)
     return lib
 
 
