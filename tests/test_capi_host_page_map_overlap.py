@@ -1,10 +1,12 @@
 """Page-map outputs that overlap inputs or one another are refused: every CTA redoes the sums over the requests, so one
 that wrote over them would change another's."""
 import pytest
+import torch
 
-import asymmetric_head_kv_b200 as ak  # noqa: F401  (the package loads the library)
+import asymmetric_head_kv_b200 as ak
 from asymmetric_head_kv_b200 import _capi
 from asymmetric_head_kv_b200.build import build
+from oracle import kv8
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -37,11 +39,27 @@ def test_overlaps_are_refused(out, other):
     assert call(**{out: high // step * step}) == _capi.INVALID_ARG
 
 
-def test_neighbours_are_not():
-    """Side by side, and the inputs among themselves, is fine: the call gets as far as looking for a device."""
-    ok = call()
-    assert ok != _capi.INVALID_ARG
-    assert call(new_lens=ARGS["seq_lens"]) == ok
-    assert call(total_lens=ARGS["seq_lens"] + 16) == ok and call(query_start=ARGS["new_lens"] - 20) == ok
-    assert call(positions=None) == ok
-    assert call(slot_map=ARGS["free_pages"] + 64) == ok
+@pytest.mark.gpu
+def test_neighbours_are_not(cuda_device):
+    """Every buffer cut from one allocation, side by side, and one tensor for both inputs: the map is right."""
+    B, cap = 4, 64
+    pool = torch.zeros(512, dtype=torch.int32, device=cuda_device)
+    at = 0
+
+    def cut(n):
+        nonlocal at
+        at += n
+        return pool[at - n:at]
+    slots, positions, lens, start, total, used, free = cut(cap), cut(cap), cut(B), cut(B + 1), cut(B), cut(1), cut(16)
+    table = cut(B * 8).view(B, 8)
+    lens.copy_(torch.tensor([3, 0, 5, 1]))
+    free.copy_(torch.arange(16, 32))
+    table[:, 0] = torch.tensor([7, 6, 5, 4])
+    word = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    ak.page_map(lens, lens, table, free, 4, 40, start, slots, positions, total, used, status=word)
+    want = kv8.page_map([3, 0, 5, 1], [3, 0, 5, 1], [[7] + [0] * 7, [6] + [0] * 7, [5] + [0] * 7, [4] + [0] * 7],
+                        range(16, 32), 4, 40, cap)
+    assert word.item() == want["status"]
+    for got, name in ((start, "query_start"), (slots, "slot_map"), (positions, "positions"), (total, "total_lens"),
+                      (used, "pages_used"), (table, "block_table")):
+        assert got.tolist() == want[name].tolist(), name
