@@ -477,7 +477,7 @@ def decode_paged_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """:func:`decode` over an 8-bit paged cache: e4m3 pools k_pages [num_pages, page_size, n_k, d_k] and v_pages
     [num_pages, page_size, n_v, d_v], scale bytes [num_pages, page_size // scale_block, heads], block_table int32
-    [B, max_blocks], seq_lens int32 [B].  Returns bf16 [B, n_q, d_v]."""
+    [B, max_blocks], seq_lens int32 [B].  n_q / n_k must be 1, 2, 4, 8 or 16.  Returns bf16 [B, n_q, d_v]."""
     if out is None or workspace is None:
         dims = _kv8_dims(q, q.shape[0], k_pages, v_pages)
         with _on(stream):

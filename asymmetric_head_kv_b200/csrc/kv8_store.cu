@@ -340,6 +340,8 @@ diffqkv_status_t kv8_store_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cac
     if (tokens < 0) return DIFFQKV_ERR_INVALID_ARG;
     if (tokens == 0) return DIFFQKV_OK;
     if (!k_new || !v_new || !slot_map) return DIFFQKV_ERR_INVALID_ARG;
+    if ((long long)d->n_k + d->n_v > 65535) return DIFFQKV_ERR_UNSUPPORTED;  // grid
+    if ((long long)tokens * std::max(d->n_k, d->n_v) * 16 > 0x7fffffffLL) return DIFFQKV_ERR_UNSUPPORTED;  // thread index
     if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(slot_map) & 3u) ||
         (reinterpret_cast<uintptr_t>(status) & 3u))
         return DIFFQKV_ERR_MISALIGNED;
@@ -371,8 +373,6 @@ diffqkv_status_t kv8_store_launch(const diffqkv_dims_t *d, const diffqkv_kv8_cac
         while (a.share < kStoreWarps && a.share * 32 * kRunVec * 8 / std::max(d->d_k, d->d_v) < a.sb &&
                (long long)tokens * (d->n_k + d->n_v) / a.sb * a.share < kWarpsPerSm * dev.num_sms)
             a.share *= 2;
-    if ((d->n_k + d->n_v) > 65535) return DIFFQKV_ERR_UNSUPPORTED;
-    if ((long long)tokens * std::max(d->n_k, d->n_v) * 16 > 0x7fffffffLL) return DIFFQKV_ERR_UNSUPPORTED;  // thread index
     if (d->d_k == 64)
         d->d_v == 64 ? store_launch<64, 64>(a, stream) : store_launch<64, 128>(a, stream);
     else

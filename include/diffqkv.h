@@ -39,7 +39,8 @@
  *    threads) report independently, and reading one word clears no other.
  *  - Supported shapes: n_q % n_k == 0, n_q % n_v == 0 (else INVALID_ARG);
  *    n_q / n_k in {1, 2, 4, 8, 16} and d_k, d_v in {64, 128} (else
- *    UNSUPPORTED).
+ *    UNSUPPORTED).  The 8-bit prefill takes any n_q / n_k, the 8-bit cache
+ *    write none (it has no query heads).
  */
 #ifndef DIFFQKV_H_
 #define DIFFQKV_H_
@@ -553,7 +554,8 @@ typedef struct {
  * block's codes and scale unspecified.  A slot >= num_pages * page_size is flagged
  * DIFFQKV_ERR_DEVICE_PAGE and skipped.  dims->batch and scale are not used (they must
  * still be valid).  tokens >= 0 (0: nothing is launched, the other pointers may be NULL).
- * num_pages * page_size must fit in int32.  device_status_word as in
+ * num_pages * page_size must fit in int32; tokens * max(n_k, n_v) must stay below 2^27 and
+ * n_k + n_v below 2^16 (else DIFFQKV_ERR_UNSUPPORTED).  device_status_word as in
  * diffqkv_prefill_causal_ex.
  */
 diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache, const void *k_new,
@@ -575,9 +577,12 @@ diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8
  * weights (times their V scales) are split into three e4m3 terms each: 12 significant
  * bits, or 2^-28 of the head's largest where that is more.  (The largest product of a
  * position's own weight and V scale, that is: blocks of large scale and little weight
- * cost the others nothing.)  All sums, maxima and weights are fp32.  Lengths, clamping, zero rows for length 0, max_seq_len, the workspace
- * (diffqkv_decode_workspace_size) and its error word are those of diffqkv_decode; entries
- * read, bad entries and shared pages those of diffqkv_decode_paged.
+ * cost the others nothing.)  All sums, maxima and weights are fp32.  Lengths, clamping,
+ * zero rows for length 0, max_seq_len, the workspace (diffqkv_decode_workspace_size) and
+ * its error word are those of diffqkv_decode; entries read, bad entries and shared pages
+ * those of diffqkv_decode_paged.  n_q / n_k must be 1, 2, 4, 8 or 16 (else
+ * DIFFQKV_ERR_UNSUPPORTED): a cache of other head counts can be written and prefilled, not
+ * decoded.
  */
 diffqkv_status_t diffqkv_decode_paged_kv8(const diffqkv_dims_t *dims, const diffqkv_kv8_cache_t *cache,
                                           const void *q, const int32_t *block_table, int32_t max_blocks,
@@ -585,8 +590,8 @@ diffqkv_status_t diffqkv_decode_paged_kv8(const diffqkv_dims_t *dims, const diff
                                           size_t workspace_bytes, diffqkv_stream_t stream);
 
 /* Bytes of workspace diffqkv_prefill_paged_kv8 needs (0 if dims are invalid); zero-filled
- * before its first use, and left reusable by every call that completes, as diffqkv_decode's (whose layout it has; the size
- * does not depend on the batch). */
+ * before its first use, and left reusable by every call that completes, as diffqkv_decode's
+ * (whose layout it has).  Does not depend on the batch. */
 size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
 
 /*
@@ -604,7 +609,8 @@ size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
  * Row r of request b sits at position seq_lens[b] - n_b + r and attends to positions 0 up
  * to its own.  Lengths outside [0, max_blocks * page_size], starts outside [0, tokens] or
  * descending, and n_b > seq_lens[b] are clamped and flagged DIFFQKV_ERR_DEVICE_SEQLEN in the
- * workspace's error word; a row without a position gets zeros.  Bad table entries as in
+ * workspace's error word; a row without a position gets zeros, and rows that such starts
+ * give to two requests are left unspecified.  Bad table entries as in
  * diffqkv_prefill_causal_paged.  Codes and queries are converted to f16 with power-of-two
  * scales (exactly, but for elements of a query row 2^31 below its largest), products are
  * summed in fp32, and softmax weights, their V scales included, are rounded to f16 for the
