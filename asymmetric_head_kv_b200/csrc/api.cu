@@ -38,6 +38,23 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+// Makes the current device's primary context current on a thread that has made no CUDA call yet: the runtime does so by
+// itself with its first launch, but the encoding of tensor maps, a driver call, comes before that and needs one.
+bool bind_context(int dev) {
+    static PFN_cuCtxGetCurrent_v4000 get = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            get = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
+    });
+    CUcontext ctx = nullptr;
+    if (!get || get(&ctx) != CUDA_SUCCESS) return false;
+    return ctx || cudaSetDevice(dev) == cudaSuccess;  // (a context that is there stays, whosever it is)
+}
+
 __global__ void wait_timeout_selftest_kernel(int32_t *status, uint64_t limit_ns) {
     __shared__ __align__(8) uint64_t bar;
     __shared__ int abort_flag;
@@ -60,6 +77,10 @@ diffqkv_status_t current_device_info(DeviceInfo *info) {
         return DIFFQKV_ERR_NO_DEVICE;
     }
     if (dev >= kMaxDevices) return DIFFQKV_ERR_UNSUPPORTED;
+    if (!bind_context(dev)) {
+        cudaGetLastError();
+        return DIFFQKV_ERR_CUDA;
+    }
     std::lock_guard<std::mutex> lock(g_dev_mutex);
     DeviceInfo &d = g_devices[dev];
     if (d.device != dev) {
