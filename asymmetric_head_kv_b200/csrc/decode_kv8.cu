@@ -35,8 +35,8 @@
 //    are zero, but the codes there may be NaN.
 //  * MMA, commit and TMA are issued by an elected lane (kv8.cuh): behind a test of the lane index the MMA warp alone
 //    took longer than a tile's bytes.
-// 16 sequences of 32768, 4 K heads of 64 and 16 V heads of 128: 201 us from pages of 16, 6.0 TB/s, 0.93 of the measured
-// copy bandwidth; 195 us from pages of 64.  32 query heads over 4 + 16 heads of 64: 3.3 TB/s, 16 + 16 heads of 128: 5.6 TB/s;
+// 16 sequences of 32768, 4 K heads of 64 and 16 V heads of 128: 205 us from pages of 16, 5.9 TB/s, 0.91 of the measured
+// copy bandwidth; 198 us from pages of 64.  32 query heads over 4 + 16 heads of 64: 3.0 TB/s, 16 + 16 heads of 128: 5.2 TB/s;
 // the fewer bytes a tile has for its heads, the more the softmax warps' time shows (about 3400 clocks a tile and CTA, two
 // CTAs an SM): exponentials, the e4m3 terms (a conversion of two values takes 4 clocks) and three shared-memory barriers.
 // One sequence of 512: 9.4 us, a chain of launch, table, TMA, two MMAs, partials and merge.

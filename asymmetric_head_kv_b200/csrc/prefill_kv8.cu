@@ -32,7 +32,8 @@
 //    Equal shares of all the work on persistent CTAs were slower, 739 us against 500 for two prompts of 8192: each
 //    further unit of a CTA costs about 10 us of pipeline, and the softmax loop inside a loop over units lacks registers.
 // What bounds it: the softmax warps, 64 exponentials a row and tile (16 a clock and SM: half of the tile's 1900 clocks) and
-// their latencies.  Two prompts of 8192, 16 heads of 64/128: 488 us, 845 TFLOP/s, 0.50 of the measured GEMM peak; four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
+// their latencies.  Two prompts of 8192, 16 heads of 64/128: 488 us, 845 TFLOP/s, 0.50 of the measured GEMM peak (tensor
+// pipe 40% busy, XU 56%, 62% of issue slots); four requests of 17 rows over 1003 positions: 20.5 us, of which about 14 are
 // one CTA's start and end.
 #include <cuda_fp16.h>
 #include <math.h>

@@ -577,7 +577,8 @@ diffqkv_status_t diffqkv_kv8_store(const diffqkv_dims_t *dims, const diffqkv_kv8
  * weights (times their V scales) are split into three e4m3 terms each: 12 significant
  * bits, or 2^-28 of the head's largest where that is more.  (The largest product of a
  * position's own weight and V scale, that is: blocks of large scale and little weight
- * cost the others nothing.)  All sums, maxima and weights are fp32.  Lengths, clamping,
+ * cost the others nothing.)  All sums, maxima and weights are fp32; a weight 2^-118 below
+ * its head's largest may count as zero, whatever its V scale.  Lengths, clamping,
  * zero rows for length 0, max_seq_len, the workspace (diffqkv_decode_workspace_size) and
  * its error word are those of diffqkv_decode; entries read, bad entries and shared pages
  * those of diffqkv_decode_paged.  n_q / n_k must be 1, 2, 4, 8 or 16 (else
@@ -615,7 +616,7 @@ size_t diffqkv_prefill_paged_kv8_workspace_size(const diffqkv_dims_t *dims);
  * scales (exactly, but for elements of a query row 2^31 below its largest), products are
  * summed in fp32, and softmax weights, their V scales included, are rounded to f16 for the
  * second product: 11 significant bits, or multiples of 2^-23 of the row's largest where
- * that is coarser.  (Tiles of 64 positions whose blocks' scales lie 2^9 apart, for V, or
+ * that is coarser; one 2^-118 below it before its V scale may count as zero.  (Tiles of 64 positions whose blocks' scales lie 2^9 apart, for V, or
  * 2^16, for K, take about five times as long.)  A NaN in a stored row reaches the query
  * rows at and behind its position (of K: the heads' whole rows, of V: its column), no others.
  * tokens >= 1.  workspace as above.
