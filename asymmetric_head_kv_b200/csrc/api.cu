@@ -253,7 +253,7 @@ const char *diffqkv_status_string(int32_t status) {
     }
 }
 
-int32_t diffqkv_version(void) { return 10300; }
+int32_t diffqkv_version(void) { return 10301; }
 
 size_t diffqkv_decode_workspace_size(const diffqkv_dims_t *dims) { return diffqkv::decode_workspace_size(dims); }
 

@@ -617,8 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n + i >= n1) break;
                 const int k = n + i - n0, slot = k % kScaleSlots;
                 if (k >= kScaleSlots)
-                    wait_for(&ms.sc_empty[slot], (uint32_t)((k / kScaleSlots - 1) & 1), a.wait_limit_ns, abort_flag,
-                                      a.status);
+                    wait_for(&ms.sc_empty[slot], (uint32_t)((k / kScaleSlots - 1) & 1), a.wait_limit_ns, abort_flag, a.status);
                 const int k0 = kv8_exp(ek[i][0]), k1 = kv8_exp(ek[i][1]), v0 = kv8_exp(ev[i][0]), v1 = kv8_exp(ev[i][1]);
                 int kr = __reduce_max_sync(0xffffffffu, max(k0, k1)), vr = __reduce_max_sync(0xffffffffu, max(v0, v1));
                 const bool mixed = kr - __reduce_min_sync(0xffffffffu, min(k0, k1)) > kSpreadK ||
